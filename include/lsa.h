@@ -70,6 +70,7 @@ typedef enum lsa_status {
 #define LSA_DEVERR_COUNT 4   /* count[r] outside [0, index_topk] */
 #define LSA_DEVERR_SEQ 8     /* seq_of_row[r] outside [0, n_seq) */
 #define LSA_DEVERR_TIMEOUT 16 /* a bounded wait inside a kernel gave up (the CTA stopped early) */
+#define LSA_DEVERR_PAGE 32   /* a block-table entry or slot outside its page pool, or no free page left */
 
 /*
  * Method constants, under the pages' config key names ([LSA-2.0] 模型架构配置;
@@ -103,6 +104,9 @@ LSA_API void lsa_config_default(lsa_config* cfg);
 #define LSA_OP_INDEX_PROJECT 6
 #define LSA_OP_MLA_DECODE_LAYER 7 /* lsa_sparse_mla_decode_layer (cfg->cli_factor sub-blocks) */
 #define LSA_OP_MTP_DECODE 8       /* lsa_mtp_mla_decode (any n_draft) */
+#define LSA_OP_FP8_INDEX 9        /* lsa_fp8_index_scores */
+#define LSA_OP_FP8_MLA 10         /* lsa_fp8_sparse_mla (cfg->cli_factor sub-blocks) */
+#define LSA_OP_FP8_FORWARD 11     /* lsa_fp8_forward */
 
 /*
  * Bytes of workspace the operation uses at full speed for these sizes (host
@@ -454,6 +458,144 @@ LSA_API lsa_status lsa_forward(const lsa_config* cfg, int32_t mode, int32_t n_ro
                        const lsa_bf16* const* latent, lsa_bf16* const* out, float* const* lse,
                        int32_t* idx_out, int32_t* count_out, void* ws, size_t ws_bytes,
                        void* stream);
+
+/*
+ * Paged 8-bit caches
+ * ------------------
+ * The entry points below serve sequences that grow: caches in pages of
+ * LSA_PAGE_TOKENS tokens, found through a block table, with every cached vector
+ * in e4m3 codes and one power-of-two fp32 scale per vector. (The pages serve
+ * from growing caches and name 4/6/8-bit weights, but give no 8-bit cache; the
+ * format and the operators are this library's own.)
+ *
+ * Quantisation of a vector x (a 576-dim latent row, a 128-dim index key or one
+ * head's 128-dim index query): a = max |x_i|; scale = the smallest power of two
+ * s with a <= 448 s, at least 2^-126 (s = 1 when a = 0); code_i = x_i / s rounded to
+ * nearest-even e4m3. x_i / s is exact, so the codes are a function of the bits
+ * of x alone. A vector holding an infinity or NaN gets scale NaN and zero
+ * codes: it stands for NaN throughout. The cached vector stands for scale * code.
+ *
+ * Latent pages: uint8 [n_pages, 64, LSA_FP8_LATENT_ROW]: a token's 576 codes,
+ *   its fp32 scale at byte 576, then 12 bytes of padding (written as zero).
+ * Key pages: uint8 [n_pages, LSA_FP8_KEY_PAGE]: 64 tokens x 128 codes, then the
+ *   64 tokens' fp32 scales at byte 8192.
+ * block_table int32 [n_seq, max_pages]: token t of sequence b lives in page
+ *   block_table[b, t / 64] at row t % 64. Latent and key pages of one layer (and
+ *   of every layer that shares the table) use the same page numbers.
+ * Slot of a token: page * 64 + row. Pools are limited to n_pages <= 2^25 - 1.
+ * Pools must be 16-byte aligned.
+ *
+ * Rows (queries): seq_of_row int32 [n_rows] (NULL: row r is sequence r) and pos
+ * int32 [n_rows]; a row sees keys 0..pos of its sequence. seq_of_row[r] = -1 marks
+ * a padding row (a fixed-size batch): it is skipped and nothing of it is
+ * written. Another number outside [0, n_seq) sets LSA_DEVERR_SEQ (no scores, or
+ * zero output with lse -inf); a position < 0, or past max_len or max_pages * 64,
+ * sets LSA_DEVERR_POS and is clamped. A page outside the pool sets
+ * LSA_DEVERR_PAGE; its keys are never read (score -inf; skipped by the attention).
+ */
+#define LSA_PAGE_TOKENS 64
+#define LSA_FP8_LATENT_ROW 592
+#define LSA_FP8_KEY_PAGE 8448
+
+/*
+ * Block tables and slot maps from the request lengths, on the device: request s
+ * holds cached[s] tokens in its first ceil(cached/64) pages and gets fresh[s]
+ * more. The pages it needs beyond those it owns are taken from free_pages in
+ * order (request by request) and written into its block-table row; entries of
+ * other columns are left as they were. The fresh tokens become rows in request
+ * order: seq_of_row, pos = cached[s] + i, slot. Array entries behind the last
+ * row are set to -1 (padding rows, which the other entry points skip).
+ *
+ * cached, fresh int32 [n_seq]; free_pages int32 [n_free]; block_table int32
+ * [n_seq, max_pages] in place; seq_of_row, pos, slot int32 [n_rows] (n_rows =
+ * the arrays' capacity); totals int32 [2]: the rows and the pages the requests
+ * need (saturated at 2^31 - 1). 1 <= n_seq <= LSA_PLAN_MAX_SEQ.
+ * totals[0] > n_rows sets LSA_DEVERR_COUNT (the rows beyond are not written);
+ * totals[1] > n_free, or a negative or too large page number met on the way,
+ * sets LSA_DEVERR_PAGE (entry and slots -1). A request with a negative length
+ * or with cached + fresh > max_pages * 64 sets LSA_DEVERR_POS and gets nothing.
+ * Running it again with the same inputs writes the same outputs.
+ */
+#define LSA_PLAN_MAX_SEQ 16384
+LSA_API lsa_status lsa_page_plan(int32_t n_seq, const int32_t* cached, const int32_t* fresh,
+                                 const int32_t* free_pages, int32_t n_free, int32_t* block_table, int32_t max_pages,
+                                 int32_t n_rows, int32_t* seq_of_row, int32_t* pos, int32_t* slot, int32_t* totals,
+                                 void* stream);
+
+/*
+ * Quantises new tokens' cache rows into their slots.
+ * slot int32 [n_rows]: -1 skips the row; a number outside [0, n_pages * 64) sets
+ * LSA_DEVERR_PAGE and skips it. Slots must be distinct (two rows of one slot
+ * leave a mix of both).
+ * n_sub (0..2) latent arrays: latent[z] bf16 rows of 576, latent_ld elements
+ * apart (>= 576, a multiple of 8), into latent_pages[z]. latent and
+ * latent_pages: HOST arrays of n_sub DEVICE pointers (NULL when n_sub is 0).
+ * k_idx bf16 rows of 128, k_ld elements apart (>= 128, a multiple of 8), into
+ * key_pages; both NULL: no index keys in this call. Arrays 16-byte aligned.
+ */
+LSA_API lsa_status lsa_fp8_append(const lsa_config* cfg, int32_t n_rows, const int32_t* slot, int32_t n_sub,
+                                  const lsa_bf16* const* latent, int64_t latent_ld, void* const* latent_pages,
+                                  const lsa_bf16* k_idx, int64_t k_ld, void* key_pages, int32_t n_pages,
+                                  void* stream);
+
+/*
+ * Lightning-indexer scores over 8-bit paged index keys: lsa_index_scores' formula,
+ * mask and forcing with each head's query quantised as above (q8, sq) and the
+ * cached keys as they stand (k8, sk):
+ *   scores[r, j] = sum_h w[r,h] * max(0, sq[r,h] * sk[j] * (q8[r,h,:] . k8[j,:]))
+ * for j <= pos[r]; forced columns +inf; other entries are not written. The
+ * products of codes are exact and summed in fp32.
+ * q_idx bf16 [n_rows, 32, 128]; w fp32 [n_rows, 32]; scores fp32 [n_rows, ld],
+ * ld >= max_len; every pos[r] < max_len. topk_hist: as lsa_index_scores.
+ * Workspace: lsa_workspace_size(LSA_OP_FP8_INDEX) (the quantised queries).
+ */
+LSA_API lsa_status lsa_fp8_index_scores(const lsa_config* cfg, int32_t n_rows, int32_t n_seq,
+                                        const int32_t* seq_of_row, const int32_t* pos, const lsa_bf16* q_idx,
+                                        const float* w, const void* key_pages, int32_t n_pages,
+                                        const int32_t* block_table, int32_t max_pages, int64_t max_len,
+                                        float* scores, int64_t ld, uint32_t* topk_hist, void* ws, size_t ws_bytes,
+                                        void* stream);
+
+/*
+ * Sparse absorbed-latent MLA over 8-bit paged latent rows, for any mix of decode
+ * and prefill rows, n_sub (1..cfg->cli_factor) sub-blocks over one selection:
+ *   x_i = softmax_scale * s_i * (q_abs[r,h,:] . c_i[:576]), i over the row's list
+ *   out[r,h,:] = sum_i softmax(x)_i * s_i * c_i[:512];  lse[r,h] = log sum_i exp(x_i)
+ * (c_i the codes and s_i the scale of the key's row). The list is idx[r, :count[r]]
+ * (int32 [n_rows, index_topk], positions in the row's sequence, in any order);
+ * idx NULL: every key 0..pos[r] (count unused). An entry outside 0..pos[r] sets
+ * LSA_DEVERR_INDEX and is skipped; a count outside [0, index_topk] sets
+ * LSA_DEVERR_COUNT and is clamped; a key listed twice counts twice. A row
+ * without keys gets output 0 and lse -inf.
+ * q_abs, latent_pages, out, lse: HOST arrays of n_sub DEVICE pointers (lse, or
+ * an entry of it, may be NULL): q_abs bf16 [n_rows, 32, 576], out bf16
+ * [n_rows, 32, 512], lse fp32 [n_rows, 32]. The query enters to its last bit
+ * (to 2^-22 of its head's largest element); the softmax weights are rounded to
+ * 8 significant bits, as a bf16 weight is. Logits, sums and outputs accumulate in fp32.
+ * Workspace optional (split-K partials): lsa_workspace_size(LSA_OP_FP8_MLA).
+ */
+LSA_API lsa_status lsa_fp8_sparse_mla(const lsa_config* cfg, int32_t n_sub, int32_t n_rows, int32_t n_seq,
+                                      const int32_t* seq_of_row, const int32_t* pos, const lsa_bf16* const* q_abs,
+                                      const void* const* latent_pages, int32_t n_pages, const int32_t* block_table,
+                                      int32_t max_pages, const int32_t* idx, const int32_t* count, int64_t max_len,
+                                      lsa_bf16* const* out, float* const* lse, void* ws, size_t ws_bytes,
+                                      void* stream);
+
+/*
+ * The whole layer over paged 8-bit caches, as lsa_forward over packed bf16 ones:
+ * lsa_fp8_index_scores, lsa_topk, then lsa_fp8_sparse_mla for the cli_factor
+ * sub-blocks. When max_len <= index_topk the indexer is not run (q_idx, w and
+ * key_pages may be NULL) and every sub-block is dense. Rows are processed in
+ * blocks that fit the workspace (lsa_workspace_size(LSA_OP_FP8_FORWARD); the
+ * minimum is one row's). idx_out int32 [n_rows, index_topk] and count_out int32
+ * [n_rows]: optional (both or neither); unwritten when dense.
+ */
+LSA_API lsa_status lsa_fp8_forward(const lsa_config* cfg, int32_t n_rows, int32_t n_seq, const int32_t* seq_of_row,
+                                   const int32_t* pos, int64_t max_len, const lsa_bf16* q_idx, const float* w,
+                                   const void* key_pages, const lsa_bf16* const* q_abs,
+                                   const void* const* latent_pages, int32_t n_pages, const int32_t* block_table,
+                                   int32_t max_pages, lsa_bf16* const* out, float* const* lse, int32_t* idx_out,
+                                   int32_t* count_out, void* ws, size_t ws_bytes, void* stream);
 
 /* Message for the last non-OK status returned on this thread ("" if none). */
 LSA_API const char* lsa_last_error(void);

@@ -7,7 +7,9 @@
 #include <algorithm>
 #include <atomic>
 
+#include "api.h"
 #include "common.cuh"
+#include "fp8.h"
 #include "kernels.h"
 
 namespace lsa {
@@ -57,14 +59,9 @@ lsa_status check_cfg(const lsa_config* c, const char* fn) {
 }
 
 namespace {
-
-constexpr size_t kAlign = 256;
 constexpr int kTopkPreferredRows = 4096;
 constexpr size_t kPrefillScoreBudget = size_t(4) << 30;  // bytes of scores per prefill block
-
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
+}  // namespace
 
 lsa_status cuda_status(cudaError_t e, const char* fn) {
   if (e == cudaSuccess) return LSA_OK;
@@ -74,7 +71,7 @@ lsa_status cuda_status(cudaError_t e, const char* fn) {
 // The top-k's workspace. Rows taken by several CTAs each also get room for the
 // threshold bin's candidates beyond the kTopkCap of the base layout: a sixteenth
 // of the row (at most 2^18), so that the bin rarely outgrows it.
-size_t topk_ws(int n_rows, int64_t max_len = 0) {
+size_t topk_ws(int n_rows, int64_t max_len) {
   size_t per = kTopkRowBytes;
   if (max_len > 0 && topk_uses_workspace(n_rows, max_len)) {
     const int64_t room = std::min<int64_t>(max_len / 16, int64_t(1) << 18);
@@ -82,6 +79,8 @@ size_t topk_ws(int n_rows, int64_t max_len = 0) {
   }
   return (size_t)std::min(n_rows, kTopkPreferredRows) * per + kAlign;
 }
+
+namespace {
 
 // Split-K workspace of the MLA launch, whichever split count it picks.
 size_t mla_ws(int n_rows, int n_sub, int64_t max_list) {
@@ -96,11 +95,15 @@ size_t forward_block_ws(const lsa_config* c, int R, int64_t max_len) {
          align_up((size_t)R * sizeof(int32_t)) + topk_ws(R, max_len) + mla_ws(R, c->cli_factor, c->index_topk);
 }
 
+}  // namespace
+
 int prefill_block_rows(int n_rows, int64_t max_len) {
   int64_t r = (int64_t)(kPrefillScoreBudget / ((size_t)max_len * sizeof(float)));
   r = std::max<int64_t>(64, r / 64 * 64);
   return (int)std::min<int64_t>(r, n_rows);
 }
+
+namespace {
 
 lsa_status run_index_scores(const lsa_config* c, int n_rows, int n_seq, const int32_t* seq_of_row,
                             int seq_identity, const int32_t* pos, const lsa_bf16* q_idx, const float* w,
@@ -149,9 +152,11 @@ lsa_status run_index_scores(const lsa_config* c, int n_rows, int n_seq, const in
   return cuda_status(launch_topk_hist_only(t, topk_hist, st), "lsa_index_scores");
 }
 
+}  // namespace
+
 lsa_status run_topk(const lsa_config* c, int n_rows, const int32_t* pos, int64_t max_len,
                     const float* scores, int64_t ld, int32_t* idx, int32_t* count, void* ws,
-                    size_t ws_bytes, cudaStream_t st, uint32_t* hist_ext = nullptr) {
+                    size_t ws_bytes, cudaStream_t st, uint32_t* hist_ext) {
   TopkArgs a;
   a.scores = scores;
   a.ld = ld;
@@ -175,6 +180,8 @@ lsa_status run_topk(const lsa_config* c, int n_rows, const int32_t* pos, int64_t
   if (st2 != LSA_OK) return st2;
   return max_len <= c->index_topk ? LSA_DENSE : LSA_OK;
 }
+
+namespace {
 
 MlaArgs mla_args(const lsa_config* c, int n_sub, int n_rows, int decode) {
   MlaArgs a = {};
@@ -279,6 +286,10 @@ size_t lsa_workspace_size(const lsa_config* c, int32_t op, int32_t n_rows, int32
       return mla_ws(n_rows, c->cli_factor, list) + kAlign;
     case LSA_OP_MTP_DECODE:
       return mla_ws(n_rows, kMaxSub, list) + kAlign;
+    case LSA_OP_FP8_INDEX:
+    case LSA_OP_FP8_MLA:
+    case LSA_OP_FP8_FORWARD:
+      return fp8_workspace_size(c, op, n_rows, std::max(n_seq, 1), max_len);
     default:
       return 0;
   }

@@ -21,8 +21,10 @@ LSA_OK, LSA_DENSE = 0, 1
 LSA_ERR_INVALID, LSA_ERR_UNSUPPORTED, LSA_ERR_WORKSPACE, LSA_ERR_CUDA, LSA_ERR_DEVICE = -1, -2, -3, -4, -5
 OP_TOPK, OP_MLA_DECODE, OP_MLA_PREFILL, OP_FORWARD_DECODE, OP_FORWARD_PREFILL = 1, 2, 3, 4, 5
 OP_INDEX_PROJECT, OP_MLA_DECODE_LAYER, OP_MTP_DECODE = 6, 7, 8
+OP_FP8_INDEX, OP_FP8_MLA, OP_FP8_FORWARD = 9, 10, 11
 TOPK_HIST_WORDS = 2056
-DEVERR_POS, DEVERR_INDEX, DEVERR_COUNT, DEVERR_SEQ, DEVERR_TIMEOUT = 1, 2, 4, 8, 16
+DEVERR_POS, DEVERR_INDEX, DEVERR_COUNT, DEVERR_SEQ, DEVERR_TIMEOUT, DEVERR_PAGE = 1, 2, 4, 8, 16, 32
+PAGE_TOKENS, FP8_LATENT_ROW, FP8_KEY_PAGE, PLAN_MAX_SEQ = 64, 592, 8448, 16384
 
 EXPORTS = (
     "lsa_config_default", "lsa_workspace_size", "lsa_index_scores", "lsa_topk",
@@ -31,6 +33,7 @@ EXPORTS = (
     "lsa_synth_rms_rows_bf16", "lsa_launch_count", "lsa_index_project", "lsa_block_summaries",
     "lsa_hier_workspace_size", "lsa_hier_select", "lsa_sparse_mla_decode_topk", "lsa_loza_mla",
     "lsa_topk_static", "lsa_sparse_mla_decode_layer", "lsa_mtp_mla_decode", "lsa_debug_arm_mla_wait_test",
+    "lsa_page_plan", "lsa_fp8_append", "lsa_fp8_index_scores", "lsa_fp8_sparse_mla", "lsa_fp8_forward",
 )
 TOPK_STATIC_MAX_ROWS = 64
 HIER_BLOCK, HIER_BLOCKS = 64, 128
@@ -100,6 +103,14 @@ def load():
     lib.lsa_hier_workspace_size.restype = _SZ
     lib.lsa_hier_select.argtypes = [ctypes.POINTER(Config), _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I32,
                                     _I32, _P, _P, _P, _SZ, _P]
+    lib.lsa_page_plan.argtypes = [_I32, _P, _P, _P, _I32, _P, _I32, _I32, _P, _P, _P, _P, _P]
+    lib.lsa_fp8_append.argtypes = [ctypes.POINTER(Config), _I32, _P, _I32, _PP, _I64, _PP, _P, _I64, _P, _I32, _P]
+    lib.lsa_fp8_index_scores.argtypes = [ctypes.POINTER(Config), _I32, _I32, _P, _P, _P, _P, _P, _I32, _P, _I32, _I64,
+                                         _P, _I64, _P, _P, _SZ, _P]
+    lib.lsa_fp8_sparse_mla.argtypes = [ctypes.POINTER(Config), _I32, _I32, _I32, _P, _P, _PP, _PP, _I32, _P, _I32, _P,
+                                       _P, _I64, _PP, _PP, _P, _SZ, _P]
+    lib.lsa_fp8_forward.argtypes = [ctypes.POINTER(Config), _I32, _I32, _P, _P, _I64, _P, _P, _P, _PP, _PP, _I32, _P,
+                                    _I32, _PP, _PP, _P, _P, _P, _SZ, _P]
     lib.lsa_last_error.argtypes = []
     lib.lsa_last_error.restype = ctypes.c_char_p
     lib.lsa_device_error.argtypes = [ctypes.POINTER(_I32)]
@@ -113,7 +124,8 @@ def load():
                  "lsa_sparse_mla_prefill", "lsa_sparse_mla_decode_layer", "lsa_mtp_mla_decode",
                  "lsa_forward", "lsa_index_project", "lsa_block_summaries", "lsa_hier_select", "lsa_device_error",
                  "lsa_sparse_mla_decode_topk", "lsa_loza_mla", "lsa_abi_version", "lsa_synth_normal_bf16",
-                 "lsa_synth_normal_f32", "lsa_synth_rms_rows_bf16"):
+                 "lsa_synth_normal_f32", "lsa_synth_rms_rows_bf16", "lsa_page_plan", "lsa_fp8_append",
+                 "lsa_fp8_index_scores", "lsa_fp8_sparse_mla", "lsa_fp8_forward"):
         getattr(lib, name).restype = _I32
     _lib = lib
     return lib
@@ -381,6 +393,173 @@ def forward(cfg, mode, seq_of_row, pos, max_len, q_idx, w, k_idx, k_off, q_abs, 
         ctypes.byref(cfg._c()), int(mode), pos.shape[0], n_seq, _ptr(seq_of_row), _ptr(pos), int(max_len),
         _ptr(q_idx), _ptr(w), _ptr(k_idx), _ptr(k_off), keep[0], keep[1], keep[2], keep[3],
         _ptr(idx_out), _ptr(count_out), _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)),
+        bind=bind, keep=keep)
+
+
+def latent_pages(n_pages, device=None) -> torch.Tensor:
+    """A zeroed pool of 8-bit latent pages (see the paged 8-bit caches in include/lsa.h)."""
+    return torch.zeros((n_pages, PAGE_TOKENS, FP8_LATENT_ROW), dtype=torch.uint8, device=device or "cuda")
+
+
+def key_pages(n_pages, device=None) -> torch.Tensor:
+    """A zeroed pool of 8-bit index-key pages."""
+    return torch.zeros((n_pages, FP8_KEY_PAGE), dtype=torch.uint8, device=device or "cuda")
+
+
+def _i32(**ts):
+    for name, t in ts.items():
+        _dt(t, torch.int32, name)
+
+
+def _len(t, n, name):
+    if t is not None and t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
+
+
+def _pools(pools, name, shape):
+    """Page pools of one call: uint8, contiguous, of one page count (returned)."""
+    n = None
+    for t in pools:
+        _dt(t, torch.uint8, name)
+        _ptr(t)
+        if tuple(t.shape[1:]) != shape or (n is not None and t.shape[0] != n):
+            raise ValueError(f"{name} must be uint8 [n_pages, {', '.join(map(str, shape))}], one n_pages per call")
+        n = t.shape[0]
+    return n
+
+
+def _shared_pages(*counts):
+    known = {n for n in counts if n is not None}
+    if len(known) > 1:
+        raise ValueError(f"page pools of one call must have the same number of pages, got {sorted(known)}")
+    return known.pop() if known else 0
+
+
+def _rows_ld(ts, width, name):
+    """Elements between the rows of bf16 [n, width] tensors whose rows may be apart."""
+    ld = None
+    for t in ts:
+        _dt(t, torch.bfloat16, name)
+        if not t.is_cuda:
+            raise ValueError("tensor must be on a CUDA device")
+        if t.dim() != 2 or t.shape[1] != width or t.stride(1) != 1:
+            raise ValueError(f"{name} must be [n_rows, {width}] with contiguous rows")
+        step = t.stride(0) if t.shape[0] > 1 else width
+        if ld is not None and step != ld:
+            raise ValueError(f"{name}: the sub-blocks must have one row stride")
+        ld = step
+    return ld
+
+
+def page_plan(cached, fresh, free_pages, block_table, seq_of_row, pos, slot, totals, stream=None, bind=False):
+    """Block tables and slot maps from request lengths (all int32): pages for the
+    requests' fresh tokens are taken from free_pages into block_table, and the
+    tokens become rows (seq_of_row, pos, slot; -1 behind the last). totals: [rows, pages]."""
+    _i32(cached=cached, fresh=fresh, free_pages=free_pages, block_table=block_table, seq_of_row=seq_of_row, pos=pos,
+         slot=slot, totals=totals)
+    n, cap = cached.numel(), seq_of_row.numel()
+    _len(fresh, n, "fresh"); _len(pos, cap, "pos"); _len(slot, cap, "slot"); _len(totals, 2, "totals")
+    if block_table.dim() != 2 or block_table.shape[0] != n:
+        raise ValueError("block_table must be [n_seq, max_pages]")
+    return _invoke(load().lsa_page_plan, (
+        n, _ptr(cached), _ptr(fresh), _ptr(free_pages), free_pages.numel(), _ptr(block_table), block_table.shape[1],
+        cap, _ptr(seq_of_row), _ptr(pos), _ptr(slot), _ptr(totals), _stream(stream)), bind=bind)
+
+
+def fp8_append(cfg, slot, latent, latent_pages, k_idx=None, key_pages=None, stream=None, bind=False):
+    """Quantises new rows into their slots: latent (a list of up to two bf16
+    [n, 576]) into latent_pages, k_idx (bf16 [n, 128], or None) into key_pages.
+    Rows may be a stride apart; slot -1 skips a row."""
+    _i32(slot=slot)
+    if len(latent) != len(latent_pages):
+        raise ValueError("latent and latent_pages must have one entry per sub-block")
+    for t in list(latent) + ([] if k_idx is None else [k_idx]):
+        if t.shape[0] != slot.numel():
+            raise ValueError("every source must have one row per slot")
+    ld = _rows_ld(latent, 576, "latent")
+    kld = None if k_idx is None else _rows_ld([k_idx], 128, "k_idx")
+    n_pages = _shared_pages(_pools(latent_pages, "latent_pages", (PAGE_TOKENS, FP8_LATENT_ROW)),
+                            _pools([] if key_pages is None else [key_pages], "key_pages", (FP8_KEY_PAGE,)))
+    keep = (_ptr_array(latent), _ptr_array(latent_pages))
+    return _invoke(load().lsa_fp8_append, (
+        ctypes.byref(cfg._c()), slot.numel(), _ptr(slot), len(latent), keep[0], ld or 576, keep[1],
+        None if k_idx is None else ctypes.c_void_p(k_idx.data_ptr()), kld or 128, _ptr(key_pages), n_pages,
+        _stream(stream)), bind=bind, keep=keep)
+
+
+def _check_rows(seq_of_row, pos, block_table):
+    _i32(seq_of_row=seq_of_row, pos=pos, block_table=block_table)
+    if seq_of_row is not None:
+        _len(seq_of_row, pos.numel(), "seq_of_row")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [n_seq, max_pages]")
+
+
+def fp8_index_scores(cfg, seq_of_row, pos, q_idx, w, key_pages, block_table, max_len, scores, ws, topk_hist=None,
+                     stream=None, bind=False):
+    """Lightning-indexer scores over 8-bit paged keys (seq_of_row None: row r is
+    sequence r; -1: a padding row, skipped)."""
+    _check_rows(seq_of_row, pos, block_table)
+    _dt(q_idx, torch.bfloat16, "q_idx"); _dt(w, torch.float32, "w"); _dt(scores, torch.float32, "scores")
+    n = pos.numel()
+    _len(q_idx, n * 32 * 128, "q_idx"); _len(w, n * 32, "w"); _len(topk_hist, n * TOPK_HIST_WORDS, "topk_hist")
+    if scores.dim() != 2 or scores.shape[0] != n:
+        raise ValueError("scores must be [n_rows, ld]")
+    n_pages = _pools([key_pages], "key_pages", (FP8_KEY_PAGE,))
+    return _invoke(load().lsa_fp8_index_scores, (
+        ctypes.byref(cfg._c()), n, block_table.shape[0], _ptr(seq_of_row), _ptr(pos), _ptr(q_idx), _ptr(w),
+        _ptr(key_pages), n_pages, _ptr(block_table), block_table.shape[1], int(max_len), _ptr(scores),
+        scores.shape[1], _ptr(topk_hist), _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)), bind=bind)
+
+
+def _sub_blocks(cfg, n, q_abs, latent_pages, out, lse):
+    k = len(q_abs)
+    if not (k == len(latent_pages) == len(out)) or (lse is not None and len(lse) != k):
+        raise ValueError("q_abs, latent_pages, out and lse must have one entry per sub-block")
+    _bf16_list(list(q_abs) + list(out), "q_abs/out")
+    for z in range(k):
+        _len(q_abs[z], n * 32 * 576, "q_abs"); _len(out[z], n * 32 * 512, "out")
+        if lse is not None and lse[z] is not None:
+            _dt(lse[z], torch.float32, "lse"); _ptr(lse[z]); _len(lse[z], n * 32, "lse")
+    pages = _pools(latent_pages, "latent_pages", (PAGE_TOKENS, FP8_LATENT_ROW))
+    keep = (_ptr_array(q_abs), _ptr_array(latent_pages), _ptr_array(out), _ptr_array(lse) if lse else None)
+    return k, pages, keep
+
+
+def fp8_sparse_mla(cfg, seq_of_row, pos, q_abs, latent_pages, block_table, idx, count, max_len, out, lse, ws=None,
+                   stream=None, bind=False):
+    """Sparse absorbed MLA over 8-bit paged latent rows, the sub-blocks of one
+    selection in one call (q_abs, latent_pages, out, lse: lists; lse or its
+    entries may be None). idx None: every visible key."""
+    _check_rows(seq_of_row, pos, block_table)
+    _i32(idx=idx, count=count)
+    n = pos.numel()
+    _len(idx, n * cfg.index_topk, "idx"); _len(count, n, "count")
+    k, n_pages, keep = _sub_blocks(cfg, n, q_abs, latent_pages, out, lse)
+    return _invoke(load().lsa_fp8_sparse_mla, (
+        ctypes.byref(cfg._c()), k, n, block_table.shape[0], _ptr(seq_of_row), _ptr(pos), keep[0], keep[1], n_pages,
+        _ptr(block_table), block_table.shape[1], _ptr(idx), _ptr(count), int(max_len), keep[2], keep[3], _ptr(ws),
+        0 if ws is None else ws.numel(), _stream(stream)), bind=bind, keep=keep)
+
+
+def fp8_forward(cfg, seq_of_row, pos, max_len, q_idx, w, key_pages, q_abs, latent_pages, block_table, out, lse, ws,
+                idx_out=None, count_out=None, stream=None, bind=False):
+    """The whole layer over paged 8-bit caches: scores, top-k, and the
+    cfg.cli_factor sub-blocks' attention (lists of cli_factor tensors)."""
+    _check_rows(seq_of_row, pos, block_table)
+    _i32(idx_out=idx_out, count_out=count_out)
+    _dt(q_idx, torch.bfloat16, "q_idx"); _dt(w, torch.float32, "w")
+    n = pos.numel()
+    _len(q_idx, n * 32 * 128, "q_idx"); _len(w, n * 32, "w")
+    _len(idx_out, n * cfg.index_topk, "idx_out"); _len(count_out, n, "count_out")
+    k, n_pages, keep = _sub_blocks(cfg, n, q_abs, latent_pages, out, lse)
+    if k != cfg.cli_factor:
+        raise ValueError(f"the layer has {cfg.cli_factor} sub-blocks, got {k}")
+    n_pages = _shared_pages(n_pages, None if key_pages is None else _pools([key_pages], "key_pages", (FP8_KEY_PAGE,)))
+    return _invoke(load().lsa_fp8_forward, (
+        ctypes.byref(cfg._c()), n, block_table.shape[0], _ptr(seq_of_row), _ptr(pos), int(max_len), _ptr(q_idx),
+        _ptr(w), _ptr(key_pages), keep[0], keep[1], n_pages, _ptr(block_table), block_table.shape[1], keep[2],
+        keep[3], _ptr(idx_out), _ptr(count_out), _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)),
         bind=bind, keep=keep)
 
 

@@ -1,0 +1,881 @@
+"""The paged 8-bit caches: page plan, quantising append, indexer scores and
+sparse MLA over 8-bit pages, against a plain 64-bit numpy statement of them
+(oracle/fp8_ref.py). CPU: the oracle's own pins and every refusal of the entry
+points. GPU: parity, masks that leave nothing, bad pages and rows, strides,
+padding, graphs, streams, offsets beyond 32 bits, and the whole run from plan to layer."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import fp8_ref as F
+from oracle import lsa_ref as R
+from sparse_attention_03_b200 import lsa
+
+gpu = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ CPU: the oracle's pins
+
+
+def test_e4m3_table_and_rounding_match_torchs_type():
+    codes = np.array([c for c in range(256) if c & 0x7F != 0x7F], dtype=np.uint8)
+    want = torch.from_numpy(codes).view(torch.float8_e4m3fn).double().numpy()
+    np.testing.assert_array_equal(F.e4m3_values(codes), want)
+    rng = np.random.default_rng(0)
+    x = np.concatenate([rng.uniform(-448, 448, 4000), rng.standard_normal(4000) * 2.0 ** rng.integers(-12, 4, 4000),
+                        (F.E4M3[1:] + F.E4M3[:-1]) / 2]).astype(np.float32)  # the ties too
+    got = F.e4m3_codes(x.astype(np.float64))
+    want = torch.from_numpy(x).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    np.testing.assert_array_equal(F.e4m3_values(got), F.e4m3_values(want))
+
+
+def test_quant_scale_is_the_smallest_power_of_two():
+    for a in (448.0, 448.0 * 2, np.nextafter(448.0, 1e9), 1.0, 1.75, 1.7500001, 2.0 ** -126, 3e38, 2.0 ** -133):
+        codes, s = F.quant(np.array([a, -a / 3, 0.0]))
+        assert a <= 448 * s and (s == 2.0 ** -126 or a > 224 * s)
+        assert abs(F.dequant(codes, s)[0] - a) <= max(a / 16, s * 2.0 ** -10)
+    codes, s = F.quant(np.zeros(5))
+    assert s == 1.0 and not codes.any()
+    codes, s = F.quant(np.array([1.0, np.inf]))
+    assert np.isnan(s) and not codes.any()
+
+
+def test_page_plan_oracle_on_a_worked_case():
+    table = np.array([[7, -1, -1], [3, 4, -1], [-1, -1, -1]])
+    t, seq, pos, slot, tot = F.page_plan([63, 128, 0], [3, 1, 0], [9, 5, 8], table, 6)
+    assert t.tolist() == [[7, 9, -1], [3, 4, 5], [-1, -1, -1]]
+    assert seq == [0, 0, 0, 1, -1, -1] and pos == [63, 64, 65, 128, -1, -1]
+    assert slot == [7 * 64 + 63, 9 * 64, 9 * 64 + 1, 5 * 64, -1, -1] and tot == [4, 2]
+
+
+# ------------------------------------------------------------------ CPU: refusals
+
+
+def _fake(n=1):
+    return ctypes.c_void_p(0x10000 * n)  # aligned, never dereferenced by the host checks
+
+
+def _fakes(k, base=1):
+    return (ctypes.c_void_p * k)(*[0x10000 * (base + i) for i in range(k)])
+
+
+def _cfg(**kw):
+    c = lsa.LsaConfig().c()
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return ctypes.byref(c)
+
+
+def test_page_plan_refusals():
+    lib = lsa.load()
+    ok = [4, _fake(1), _fake(2), _fake(3), 10, _fake(4), 8, 16, _fake(5), _fake(6), _fake(7), _fake(8), None]
+
+    def call(**at):
+        a = list(ok)
+        for i, v in at.items():
+            a[int(i[1:])] = v
+        return lib.lsa_page_plan(*a)
+
+    assert call(_0=0) == lsa.LSA_ERR_INVALID
+    assert call(_0=lsa.PLAN_MAX_SEQ + 1) == lsa.LSA_ERR_UNSUPPORTED
+    assert call(_4=-1) == lsa.LSA_ERR_INVALID
+    assert call(_6=0) == lsa.LSA_ERR_INVALID
+    assert call(_7=-1) == lsa.LSA_ERR_INVALID
+    for i in (1, 2, 3, 5, 8, 9, 10, 11):
+        assert call(**{f"_{i}": None}) == lsa.LSA_ERR_INVALID, i
+    assert b"lsa_page_plan" in lib.lsa_last_error()
+
+
+def test_append_refusals():
+    lib = lsa.load()
+    ok = [_cfg(), 4, _fake(1), 2, _fakes(2, 2), 576, _fakes(2, 4), _fake(6), 128, _fake(7), 100, None]
+
+    def call(**at):
+        a = list(ok)
+        for i, v in at.items():
+            a[int(i[1:])] = v
+        return lib.lsa_fp8_append(*a)
+
+    assert call(_0=None) == lsa.LSA_ERR_INVALID
+    assert call(_0=_cfg(n_heads=16)) == lsa.LSA_ERR_UNSUPPORTED
+    for i, bad in ((1, -1), (3, 3), (3, -1), (5, 575), (5, 580), (8, 127), (8, 132), (10, 0), (10, 2 ** 25)):
+        assert call(**{f"_{i}": bad}) == lsa.LSA_ERR_INVALID, (i, bad)
+    for i in (2, 4, 6, 7, 9):
+        assert call(**{f"_{i}": None}) == lsa.LSA_ERR_INVALID, i
+    assert call(_3=0, _7=None, _9=None) == lsa.LSA_ERR_INVALID          # nothing to append
+    assert call(_4=(ctypes.c_void_p * 2)(0x10000, None)) == lsa.LSA_ERR_INVALID
+    assert call(_6=(ctypes.c_void_p * 2)(0x10000, 0x10008)) == lsa.LSA_ERR_INVALID
+    assert call(_7=ctypes.c_void_p(0x10008)) == lsa.LSA_ERR_INVALID
+    assert call(_1=0, _2=None) == lsa.LSA_OK                             # no rows: nothing happens
+
+
+def test_index_scores_refusals():
+    lib = lsa.load()
+    ok = [_cfg(), 4, 4, _fake(1), _fake(2), _fake(3), _fake(4), _fake(5), 100, _fake(6), 8, 500, _fake(7), 512,
+          None, _fake(8), 1 << 30, None]
+
+    def call(**at):
+        a = list(ok)
+        for i, v in at.items():
+            a[int(i[1:])] = v
+        return lib.lsa_fp8_index_scores(*a)
+
+    assert call(_0=_cfg(index_head_dim=64)) == lsa.LSA_ERR_UNSUPPORTED
+    for i, bad in ((1, -1), (2, 0), (8, 0), (8, 2 ** 25), (10, 0), (11, 0), (11, 2 ** 31 + 1), (13, 499)):
+        assert call(**{f"_{i}": bad}) == lsa.LSA_ERR_INVALID, (i, bad)
+    for i in (4, 5, 6, 7, 9, 12):
+        assert call(**{f"_{i}": None}) == lsa.LSA_ERR_INVALID, i
+    assert call(_1=5, _3=None) == lsa.LSA_ERR_INVALID                    # more rows than sequences, unmapped
+    for i in (5, 6, 7, 14):
+        assert call(**{f"_{i}": ctypes.c_void_p(0x10004)}) == lsa.LSA_ERR_INVALID, i
+    assert call(_1=0, _4=None) == lsa.LSA_OK
+    n = lsa.workspace_size(lsa.LsaConfig(), lsa.OP_FP8_INDEX, 4096, 1, 16384)
+    if n > 256:  # the block form needs its quantised queries
+        assert call(_1=4096, _2=1, _15=None, _16=0) == lsa.LSA_ERR_WORKSPACE
+
+
+def test_sparse_mla_and_forward_refusals():
+    lib = lsa.load()
+    ok = [_cfg(), 2, 4, 4, _fake(1), _fake(2), _fakes(2, 3), _fakes(2, 5), 100, _fake(7), 8, _fake(8), _fake(9), 500,
+          _fakes(2, 10), None, None, 0, None]
+
+    def call(**at):
+        a = list(ok)
+        for i, v in at.items():
+            a[int(i[1:])] = v
+        return lib.lsa_fp8_sparse_mla(*a)
+
+    assert call(_0=_cfg(softmax_scale=0.0)) == lsa.LSA_ERR_INVALID
+    assert call(_0=_cfg(cli_factor=3)) == lsa.LSA_ERR_UNSUPPORTED
+    for i, bad in ((1, 0), (1, 3), (2, -1), (3, 0), (8, 0), (10, 0), (13, 0)):
+        assert call(**{f"_{i}": bad}) == lsa.LSA_ERR_INVALID, (i, bad)
+    assert call(_0=_cfg(cli_factor=1), _1=2) == lsa.LSA_ERR_INVALID
+    for i in (5, 6, 7, 9, 12, 14):
+        assert call(**{f"_{i}": None}) == lsa.LSA_ERR_INVALID, i
+    assert call(_7=(ctypes.c_void_p * 2)(0x10000, 0x10008)) == lsa.LSA_ERR_INVALID
+    assert call(_2=5, _4=None) == lsa.LSA_ERR_INVALID
+    assert call(_2=0) == lsa.LSA_OK
+
+    ok2 = [_cfg(), 4, 4, _fake(1), _fake(2), 5000, _fake(3), _fake(4), _fake(5), _fakes(2, 6), _fakes(2, 8), 100,
+           _fake(10), 90, _fakes(2, 11), None, None, None, _fake(13), 1 << 30, None]
+
+    def fwd(**at):
+        a = list(ok2)
+        for i, v in at.items():
+            a[int(i[1:])] = v
+        return lib.lsa_fp8_forward(*a)
+
+    for i in (4, 6, 7, 8, 9, 10, 12, 14):
+        assert fwd(**{f"_{i}": None}) == lsa.LSA_ERR_INVALID, i
+    assert fwd(_16=_fake(14)) == lsa.LSA_ERR_INVALID                     # idx_out without count_out
+    assert fwd(_18=None, _19=0) == lsa.LSA_ERR_WORKSPACE
+    assert fwd(_19=1000) == lsa.LSA_ERR_WORKSPACE
+    assert fwd(_1=0) == lsa.LSA_OK
+
+
+def test_workspace_sizes():
+    cfg = lsa.LsaConfig()
+    assert lsa.workspace_size(cfg, lsa.OP_FP8_FORWARD, 16, 16, 131072) >= 16 * 131072 * 4
+    assert lsa.workspace_size(cfg, lsa.OP_FP8_FORWARD, 16, 16, 2000) < 16 * 131072 * 4
+    for op in (lsa.OP_FP8_INDEX, lsa.OP_FP8_MLA, lsa.OP_FP8_FORWARD):
+        assert lsa.workspace_size(cfg, op, 0, 1, 100) == 256
+        assert lsa.workspace_size(cfg, op, -1, 1, 100) == 0
+
+
+def test_binding_refuses_wrong_tensors_on_the_cpu():
+    cfg = lsa.LsaConfig()
+    i = torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(TypeError):
+        lsa.page_plan(i.long(), i, i, i.view(4, 1), i, i, i, i[:2])
+    with pytest.raises(ValueError):
+        lsa.page_plan(i, i[:3], i, i.view(4, 1), i, i, i, i[:2])
+    with pytest.raises(ValueError):                                      # not on a CUDA device
+        lsa.page_plan(i, i, i, i.view(4, 1), i, i, i, i[:2])
+    with pytest.raises(TypeError):
+        lsa.fp8_index_scores(cfg, i, i, torch.zeros(4, 32, 128), torch.zeros(4, 32), None, i.view(4, 1), 10, None, None)
+
+
+# ------------------------------------------------------------------ GPU helpers
+
+CFG = lsa.LsaConfig  # short
+
+
+def _bf16(x):
+    return torch.from_numpy(np.asarray(x, dtype=np.float32)).bfloat16()
+
+
+def _vals(t):
+    return t.double().cpu().numpy()
+
+
+def _i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+class Caches:
+    """Sequences of given lengths in shuffled pages: pools, block table, and the
+    values the codes stand for (per sequence)."""
+
+    def __init__(self, lens, seed=0, cli=1, extra_pages=3, first_page=0, key_scale=1.0, lat_scale=1.0):
+        rng = np.random.default_rng(seed)
+        per = [-(-n // F.PAGE) for n in lens]
+        n_pages = sum(per) + extra_pages
+        order = rng.permutation(n_pages) + first_page
+        self.n_pages = n_pages + first_page
+        self.table = np.full((len(lens), max(per)), -1, dtype=np.int64)
+        self.lens, self.keys, self.lat = lens, [], [[] for _ in range(cli)]
+        at = 0
+        for s, n in enumerate(per):
+            self.table[s, :n] = order[at:at + n]
+            at += n
+        self.key_pages = lsa.key_pages(self.n_pages)
+        self.latent_pages = [lsa.latent_pages(self.n_pages) for _ in range(cli)]
+        for s, n in enumerate(lens):
+            k = rng.standard_normal((n, F.KEY)) * key_scale * 2.0 ** rng.integers(-4, 4, (n, 1))
+            c, sc = F.quant(_vals(_bf16(k)))
+            self.keys.append(F.dequant(c, sc))
+            self._put_keys(s, c, sc)
+            for z in range(cli):
+                x = rng.standard_normal((n, F.LAT)) * lat_scale * 2.0 ** rng.integers(-3, 2, (n, 1))
+                c, sc = F.quant(_vals(_bf16(x)))
+                self.lat[z].append(F.dequant(c, sc))
+                self._put_lat(z, s, c, sc)
+        self.block_table = _i32(self.table)
+
+    def slots(self, s, n):
+        t = np.arange(n)
+        return torch.from_numpy(self.table[s][t // F.PAGE] * F.PAGE + t % F.PAGE).cuda()
+
+    def _put_keys(self, s, c, sc):
+        sl = self.slots(s, len(c))
+        pg, row = sl // F.PAGE, sl % F.PAGE
+        codes = self.key_pages[:, :8192].view(-1, F.PAGE, F.KEY)
+        codes[pg, row] = torch.from_numpy(c).cuda()
+        self.key_pages.view(torch.float32)[pg, 2048 + row] = torch.from_numpy(sc).float().cuda()
+
+    def _put_lat(self, z, s, c, sc):
+        flat = self.latent_pages[z].view(-1, F.LAT_ROW)
+        sl = self.slots(s, len(c))
+        flat[sl, :F.LAT] = torch.from_numpy(c).cuda()
+        flat.view(torch.float32)[sl, F.LAT // 4] = torch.from_numpy(sc).float().cuda()
+
+
+def _score_case(lens, rows, cfg, seed=0, n_seq_of=None, hist=False, max_len=None, ld_extra=0, caches=None, scale=1.0):
+    """Runs the indexer for rows [(seq, pos)] and checks every written and unwritten entry."""
+    rng = np.random.default_rng(seed + 1)
+    c = caches or Caches(lens, seed)
+    n, max_len = len(rows), max_len or max(lens)
+    q = _bf16(rng.standard_normal((n, 32, 128)) * scale).cuda()
+    w = torch.from_numpy((rng.standard_normal((n, 32)) / 32 ** 0.5).astype(np.float32)).cuda()
+    seq, pos = _i32([r[0] for r in rows]), _i32([r[1] for r in rows])
+    scores = torch.full((n, max_len + ld_extra), 7.0, device="cuda")
+    ws = lsa.workspace(cfg, lsa.OP_FP8_INDEX, n, len(lens), max_len)
+    h = lsa.topk_hist_buffer(n) if hist else None
+    lsa.fp8_index_scores(cfg, None if n_seq_of == "identity" else seq, pos, q, w, c.key_pages, c.block_table, max_len,
+                         scores, ws, topk_hist=h)
+    err = lsa.device_error()
+    got = scores.double().cpu().numpy()
+    ocfg = R.LsaConfig(index_topk=cfg.index_topk, index_init_tokens=cfg.index_init_tokens,
+                       index_local_tokens=cfg.index_local_tokens)
+    qv, wv = _vals(q), w.double().cpu().numpy()
+    for r, (s, p) in enumerate(rows):
+        if s < 0:
+            assert (got[r] == 7.0).all(), "a padding row was written"
+            continue
+        want = F.score_row(qv[r], wv[r], c.keys[s], p, ocfg)
+        # fp32 sums of exact products: 128 truncated additions at most 2^-23 of the absolute sum each, then the
+        # 32 heads' weighted sum (two roundings a head, 2^-24 each)
+        qc, qs = F.quant(qv[r])
+        mag = np.abs(F.dequant(qc, qs)) @ np.abs(c.keys[s][:p + 1]).T          # [32, n]
+        tol = (np.abs(wv[r])[:, None] * mag).sum(0) * (128 * 2.0 ** -23 + 66 * 2.0 ** -24) + 1e-37
+        fin = np.isfinite(want)
+        np.testing.assert_array_equal(got[r, :p + 1][~fin], want[~fin])
+        assert (np.abs(got[r, :p + 1][fin] - want[fin]) <= tol[fin]).all(), (r, s, p)
+        assert (got[r, p + 1:] == 7.0).all(), "an entry past the row's position was written"
+    return err, scores, pos, h, c
+
+
+def _mla_tol(q, c_val, keys, weights, out, scale):
+    """Bounds of the kernel's roundings: the output's bf16 (half a step, 2^-8 relative), the weights' two 4-bit
+    pieces (2^-8), the flush of weights below 2^-19 of the largest, and the logits' fp32 sums of 576 exact
+    products (a truncated addition loses 2^-23 of the absolute sum) with the query's split (2^-22 of the head's
+    largest element): delta, once in a weight and once in the sum."""
+    c = c_val[np.asarray(keys)]
+    delta = scale * (577 * 2.0 ** -23 * (np.abs(q) @ np.abs(c).T)
+                     + 2.0 ** -22 * np.abs(q).max(1)[:, None] * np.abs(c).sum(1)[None]).max(1) + 2.0 ** -18
+    v = np.abs(c[:, :512])
+    tol = 2.0 ** -8 * np.abs(out) + (2.0 ** -8 + 2 * delta[:, None] + 2.0 ** -16) * (weights @ v) \
+        + 2.0 ** -19 * weights.max(1, keepdims=True) * v.sum(0)[None] + 1e-37
+    return tol, delta + 2.0 ** -18
+
+
+def _mla_case(c, rows, lists, cfg, seed=0, topk=None, q_scale=1.0, identity=False, ws="full", max_len=None, want_err=0,
+              keep=None):
+    """lists: per row its key list, or None for idx NULL (dense)."""
+    rng = np.random.default_rng(seed + 2)
+    n, n_sub, K = len(rows), len(c.lat), cfg.index_topk
+    q = [_bf16(rng.standard_normal((n, 32, 576)) * q_scale).cuda() for _ in range(n_sub)]
+    seq, pos = _i32([r[0] for r in rows]), _i32([r[1] for r in rows])
+    idx = cnt = None
+    if lists is not None:
+        ih = np.full((n, K), -5, dtype=np.int64)
+        for r, l in enumerate(lists):
+            ih[r, :len(l)] = l
+        idx, cnt = _i32(ih), _i32([len(l) for l in lists])
+    out = [torch.full((n, 32, 512), 9.0, dtype=torch.bfloat16, device="cuda") for _ in range(n_sub)]
+    lse = [torch.full((n, 32), 9.0, device="cuda") for _ in range(n_sub)]
+    max_len = max_len or max(c.lens)
+    w = lsa.workspace(cfg, lsa.OP_FP8_MLA, n, len(c.lens), max_len) if ws == "full" else ws
+    lsa.fp8_sparse_mla(cfg, None if identity else seq, pos, q, c.latent_pages, c.block_table, idx, cnt, max_len, out,
+                       lse, w)
+    assert lsa.device_error() == want_err
+    for z in range(n_sub):
+        qv, o, l = _vals(q[z]), _vals(out[z]), lse[z].double().cpu().numpy()
+        for r, (s, p) in enumerate(rows):
+            if s == -1:
+                assert (o[r] == 9.0).all() and (l[r] == 9.0).all(), "a padding row was written"
+                continue
+            keys = list(range(p + 1)) if lists is None else list(lists[r])
+            keys = [k for k in keys if 0 <= k <= p and (keep is None or keep(s, k))]
+            if s < 0 or not keys:
+                assert (o[r] == 0).all() and np.isneginf(l[r]).all()
+                continue
+            want, wl, wt = F.attend(qv[r], c.lat[z][s], keys, cfg.softmax_scale)
+            tol, ltol = _mla_tol(qv[r], c.lat[z][s], keys, wt, want, cfg.softmax_scale)
+            assert (np.abs(l[r] - wl) <= ltol).all(), (z, r, np.abs(l[r] - wl).max())
+            assert (np.abs(o[r] - want) <= tol).all(), (z, r, (np.abs(o[r] - want) / tol).max())
+    return out, lse
+
+
+def _random_lists(rows, topk, rng, full=True):
+    out = []
+    for s, p in rows:
+        m = min(p + 1, topk) if full else int(rng.integers(0, min(p + 1, topk) + 1))
+        out.append([] if s < 0 else rng.permutation(p + 1)[:m].tolist())
+    return out
+
+
+# ------------------------------------------------------------------ GPU: plan
+
+
+@gpu
+@pytest.mark.parametrize("n_seq,hi,fresh_hi,cap_extra", [(1, 1, 1, 0), (1, 200, 130, 3), (5, 64, 1, 0), (33, 500, 70, 9),
+                                                         (1000, 300, 5, 0), (1025, 130, 2, 1), (4100, 70, 3, 50),
+                                                         (16384, 65, 2, 0)])
+def test_page_plan(n_seq, hi, fresh_hi, cap_extra):
+    rng = np.random.default_rng(n_seq + hi)
+    cached = rng.integers(0, hi + 1, n_seq)
+    fresh = rng.integers(0, fresh_hi + 1, n_seq)
+    width = -(-(hi + fresh_hi) // 64) + 1
+    pool = rng.permutation(n_seq * width + 7)
+    table = np.full((n_seq, width), -1, dtype=np.int64)
+    at = 0
+    for s in range(n_seq):
+        m = -(-int(cached[s]) // 64)
+        table[s, :m] = pool[at:at + m]
+        at += m
+    free = pool[at:]
+    cap = int(fresh.sum()) + cap_extra
+    want = F.page_plan(cached, fresh, free, table, cap)
+    bt, totals = _i32(table), _i32([5, 5])
+    seq, pos, slot = (torch.full((cap,), 77, dtype=torch.int32, device="cuda") for _ in range(3))
+    for _ in range(2):  # the same inputs give the same outputs
+        lsa.page_plan(_i32(cached), _i32(fresh), _i32(free), bt, seq, pos, slot, totals)
+        assert lsa.device_error() == 0
+        np.testing.assert_array_equal(bt.cpu().numpy(), want[0])
+        for got, exp in zip((seq, pos, slot, totals), want[1:]):
+            np.testing.assert_array_equal(got.cpu().numpy(), exp)
+
+
+@gpu
+def test_page_plan_runs_out_of_room():
+    cached, fresh = _i32([10, -1, 200, 60, 0]), _i32([60, 4, 1, 10, 65])
+    table = np.full((5, 3), -1)
+    table[0, 0], table[2, :] = 1, (2, 3, 4)
+    table[3, 0] = -7                                     # a page the caller should own, but does not
+    free = np.array([11, 2 ** 25])                       # one good page, one past any pool
+    bt = _i32(table)
+    seq, pos, slot, totals = _i32([0] * 100), _i32([0] * 100), _i32([0] * 100), _i32([0, 0])
+    lsa.page_plan(cached, fresh, _i32(free), bt, seq, pos, slot, totals)
+    assert lsa.device_error() == lsa.DEVERR_POS | lsa.DEVERR_COUNT | lsa.DEVERR_PAGE
+    c2, f2 = [10, -1, 200, 60, 0], [60, 4, 1, 10, 65]
+    want = F.page_plan(c2, f2, free, table, 100)
+    np.testing.assert_array_equal(seq.cpu().numpy(), want[1])
+    np.testing.assert_array_equal(pos.cpu().numpy(), want[2])
+    np.testing.assert_array_equal(slot.cpu().numpy(), want[3])
+    np.testing.assert_array_equal(totals.cpu().numpy(), want[4])
+    got = bt.cpu().numpy()
+    assert got[0].tolist() == [1, 11, -1] and got[2].tolist() == [2, 3, 4] and got[4].tolist()[:2] == [-1, -1]
+
+
+# ------------------------------------------------------------------ GPU: append
+
+
+def _append_rows(rng, n, d):
+    x = rng.standard_normal((n, d)) * 2.0 ** rng.integers(-20, 20, (n, 1)).astype(np.float64)
+    x[1 % n] = 0.0
+    if n > 8:
+        x[2] = 448.0 / 2 ** 30
+        x[3, 0] = np.inf
+        x[4, d - 1] = np.nan
+        x[5] *= 1e38 / np.abs(x[5]).max()
+        x[6] *= 1e-39 / np.abs(x[6]).max()               # bf16 subnormals: the scale stops at 2^-126
+        x[7, ::2] *= 2.0 ** -30                           # elements far below the row's largest
+    return _bf16(x)
+
+
+@gpu
+@pytest.mark.parametrize("n,n_sub,gap,keys", [(1, 1, 0, True), (1, 0, 0, True), (9, 2, 8, True), (64, 2, 0, False),
+                                              (333, 1, 64, True), (1000, 2, 24, True)])
+def test_append_codes_and_scales_bit_for_bit(n, n_sub, gap, keys):
+    rng = np.random.default_rng(n)
+    n_pages = -(-n // 64) + 2
+    slot = rng.permutation(n_pages * 64)[:n]
+    if n > 20:
+        slot[::7] = -1
+    def wide(d):  # rows `gap` elements apart, and the bits as fp64 values
+        x = _append_rows(rng, n, d)
+        y = torch.full((n, d + gap), 3.0, dtype=torch.bfloat16)
+        y[:, :d] = x
+        return y.cuda()[:, :d], x.double().numpy()
+    lat = [wide(576) for _ in range(n_sub)]
+    key = wide(128) if keys else None
+    lp = [torch.full((n_pages, 64, 592), 0xAB, dtype=torch.uint8, device="cuda") for _ in range(n_sub)]
+    kp = torch.full((n_pages, 8448), 0xAB, dtype=torch.uint8, device="cuda") if keys else None
+    lsa.fp8_append(lsa.LsaConfig(), _i32(slot), [x[0] for x in lat], lp, key[0] if keys else None, kp)
+    assert lsa.device_error() == 0
+
+    def bits(s):
+        return s.astype(np.float32).view(np.uint32)
+
+    live = slot >= 0
+    for z in range(n_sub):
+        c, s = F.quant(lat[z][1])
+        want = np.full((n_pages * 64, 592), 0xAB, dtype=np.uint8)
+        want[slot[live], :576] = c[live]
+        want[slot[live], 576:580] = s.astype(np.float32)[live, None].view(np.uint8)
+        want[slot[live], 580:] = 0
+        got = lp[z].view(-1, 592).cpu().numpy().copy()
+        nan = np.isnan(s) & live
+        assert np.isnan(got[slot[nan], 576:580].copy().view(np.float32)).all()
+        got[slot[nan], 576:580] = want[slot[nan], 576:580]
+        neg0 = ((got ^ want) == 0x80) & ((want & 0x7F) == 0)   # the sign of a zero is kept as torch keeps it
+        np.testing.assert_array_equal(np.where(neg0, want, got), want)
+    if keys:
+        c, s = F.quant(key[1])
+        got = kp.cpu().numpy()
+        codes = got[:, :8192].reshape(-1, 128)
+        sc = got[:, 8192:].copy().view(np.float32).reshape(-1)
+        np.testing.assert_array_equal(F.e4m3_values(codes[slot[live]]), F.e4m3_values(c[live]))
+        np.testing.assert_array_equal(sc[slot[live]], s[live].astype(np.float32))
+        rest = np.setdiff1d(np.arange(n_pages * 64), slot[live])
+        assert (codes[rest] == 0xAB).all() and (sc.view(np.uint32)[rest] == 0xABABABAB).all()
+
+
+@gpu
+def test_append_flags_slots_outside_the_pool():
+    lp = [lsa.latent_pages(2)]
+    x = torch.ones(4, 576, dtype=torch.bfloat16, device="cuda")
+    lsa.fp8_append(lsa.LsaConfig(), _i32([128, -2, 127, 2 ** 31 - 1]), [x], lp)
+    assert lsa.device_error() == lsa.DEVERR_PAGE
+    rows = lp[0].view(-1, 592).cpu().numpy()
+    assert rows[127, :576].all() and not rows[:127].any()
+
+
+# ------------------------------------------------------------------ GPU: scores
+
+
+TINY = dict(index_topk=8, index_init_tokens=2, index_local_tokens=4)
+
+
+@gpu
+@pytest.mark.parametrize("hist", [False, True])
+@pytest.mark.parametrize("lens", [[1], [63], [64, 65], [1, 127, 128, 129], [300, 5, 2049, 700]])
+def test_scores_decode(lens, hist):
+    rows = [(s, n - 1) for s, n in enumerate(lens)]
+    for cfg in (lsa.LsaConfig(), lsa.LsaConfig(**TINY)):
+        err, scores, pos, h, _ = _score_case(lens, rows, cfg, hist=hist, ld_extra=3)
+        assert err == 0
+        if hist:  # the histogram is the top-k's own first pass over these scores
+            for r, (s, p) in enumerate(rows):
+                bins = h[r, :2048].cpu().numpy()
+                lo, hi = cfg.index_init_tokens, p + 1 - cfg.index_local_tokens
+                want = np.zeros(2048, dtype=np.int64)
+                if p + 1 > cfg.index_topk and hi > lo:
+                    f = scores[r, lo:hi].cpu().numpy().copy()
+                    f[f == 0] = 0.0
+                    u = f.view(np.uint32)
+                    key = np.where(u & 0x80000000, ~u, u | 0x80000000)
+                    np.add.at(want, key >> 21, 1)
+                np.testing.assert_array_equal(bins, want)
+                assert not h[r, 2048:].cpu().numpy().any()
+
+
+@gpu
+def test_scores_rows_without_a_map_are_the_sequences():
+    lens = [200, 64, 130]
+    assert _score_case(lens, [(s, n - 1) for s, n in enumerate(lens)], lsa.LsaConfig(**TINY), n_seq_of="identity")[0] == 0
+
+
+@gpu
+@pytest.mark.parametrize("lens,new,pad", [([40], 40, 0), ([300], 37, 2), ([129, 700], 64, 5), ([17, 20, 260, 33], 17, 0),
+                                          ([1500], 129, 1)])
+def test_scores_rows_of_prompts(lens, new, pad):
+    # many rows of few sequences (blocks of rows share key tiles; a block may span sequences and end in padding)
+    rows = [(s, p) for s, n in enumerate(lens) for p in range(max(0, n - new), n)] + [(-1, -1)] * pad
+    for cfg in (lsa.LsaConfig(**TINY), lsa.LsaConfig(index_topk=64, index_init_tokens=0, index_local_tokens=0)):
+        err, *_ = _score_case(lens, rows, cfg, seed=len(lens), max_len=max(lens) + 11)
+        assert err == 0
+
+
+@gpu
+def test_scores_padding_between_rows_and_unordered_positions():
+    rng = np.random.default_rng(5)
+    lens = [200, 333]
+    rows = [(int(s), int(rng.integers(0, lens[s]))) if i % 5 else (-1, -1) for i, s in enumerate(rng.integers(0, 2, 70))]
+    assert _score_case(lens, rows, lsa.LsaConfig(**TINY))[0] == 0
+
+
+@gpu
+@pytest.mark.parametrize("scale", [2.0 ** -60, 2.0 ** 40])
+def test_scores_far_from_one(scale):
+    lens = [150, 90]
+    c = Caches(lens, 3, key_scale=scale)
+    assert _score_case(lens, [(0, 149), (1, 89)], lsa.LsaConfig(**TINY), caches=c)[0] == 0
+    rows = [(0, p) for p in range(100, 150)]
+    assert _score_case(lens, rows, lsa.LsaConfig(**TINY), caches=c, scale=1 / scale)[0] == 0
+
+
+@gpu
+@pytest.mark.parametrize("many", [False, True])
+def test_scores_bad_rows_and_pages(many):
+    cfg = lsa.LsaConfig(**TINY)
+    lens = [300, 128]
+    c = Caches(lens, 1)
+    bad = c.table.copy()
+    bad[0, 2] = -1
+    bad[0, 3] = c.n_pages
+    c.block_table = _i32(bad)
+    base = [(0, 299), (0, 130), (1, 127), (7, 5), (-2, 3), (1, 400)]
+    rows = base + ([(0, 290)] * 60 if many else [])
+    n = len(rows)
+    rng = np.random.default_rng(0)
+    q = _bf16(rng.standard_normal((n, 32, 128))).cuda()
+    w = torch.from_numpy(rng.standard_normal((n, 32)).astype(np.float32)).cuda()
+    scores = torch.full((n, 320), 7.0, device="cuda")
+    ws = lsa.workspace(cfg, lsa.OP_FP8_INDEX, n, 2, 320)
+    lsa.fp8_index_scores(cfg, _i32([r[0] for r in rows]), _i32([r[1] for r in rows]), q, w, c.key_pages, c.block_table,
+                         320, scores, ws)
+    assert lsa.device_error() == lsa.DEVERR_PAGE | lsa.DEVERR_SEQ | lsa.DEVERR_POS
+    got = scores.cpu().numpy()
+    assert np.isneginf(got[0, 128:256]).all() and np.isfinite(got[0, 2:128]).all() and np.isinf(got[0, 296:300]).all()
+    assert np.isfinite(got[1, 2:127]).all() and np.isposinf(got[1, 127:131]).all()
+    assert np.isfinite(got[2, 2:124]).all()
+    assert (got[3] == 7.0).all() and (got[4] == 7.0).all()
+    ok = F.score_row(_vals(q)[2], w.double().cpu().numpy()[2], c.keys[1], 127, R.LsaConfig(8, 2, 4))
+    assert np.allclose(got[2, 2:124], ok[2:124], rtol=1e-3, atol=1e-3)
+
+
+@gpu
+@pytest.mark.parametrize("many", [False, True])
+def test_scores_of_non_finite_vectors_count_as_zero(many):
+    # max(0, NaN) is 0, as in the bf16 indexer: a key or a query head that stands for NaN adds nothing
+    cfg = lsa.LsaConfig(index_topk=8, index_init_tokens=0, index_local_tokens=1)
+    c = Caches([200], 2)
+    flat = c.key_pages.view(torch.float32)
+    flat[int(c.table[0, 1]), 2048 + 5] = float("nan")    # key 69
+    n = 40 if many else 1
+    q = _bf16(np.random.default_rng(1).standard_normal((n, 32, 128))).cuda()
+    q[:, 3, 17] = float("inf")
+    w = torch.ones(n, 32, device="cuda")
+    scores = torch.zeros(n, 200, device="cuda")
+    ws = lsa.workspace(cfg, lsa.OP_FP8_INDEX, n, 1, 200)
+    lsa.fp8_index_scores(cfg, _i32([0] * n), _i32([199] * n), q, w, c.key_pages, c.block_table, 200, scores, ws)
+    assert lsa.device_error() == 0
+    got = scores[:, :199].double().cpu().numpy()
+    assert np.isfinite(got).all() and (got[:, 69] == 0).all()
+    qv = _vals(q)
+    qv[:, 3] = 0
+    for r in (0, n - 1):
+        want = F.score_row(qv[r], np.ones(32), c.keys[0], 199, R.LsaConfig(8, 0, 1))[:199]
+        want[69] = 0
+        assert np.allclose(got[r], want, rtol=1e-4, atol=1e-4 * np.abs(want).max())
+
+
+# ------------------------------------------------------------------ GPU: attention
+
+
+@gpu
+@pytest.mark.parametrize("lens", [[1], [2, 64], [65, 128, 127], [129, 700, 33, 2049]])
+@pytest.mark.parametrize("dense", [False, True])
+def test_mla_decode(lens, dense):
+    rng = np.random.default_rng(len(lens))
+    c = Caches(lens, 4, cli=2)
+    rows = [(s, n - 1) for s, n in enumerate(lens)]
+    cfg = lsa.LsaConfig()
+    _mla_case(c, rows, None if dense else _random_lists(rows, 2048, rng), cfg)
+    _mla_case(c, rows, None if dense else _random_lists(rows, 2048, rng), cfg, identity=True, ws=None)
+
+
+@gpu
+@pytest.mark.parametrize("topk,full", [(2048, True), (2048, False), (130, True), (9, True), (129, False)])
+def test_mla_prompt_rows_padding_and_short_lists(topk, full):
+    rng = np.random.default_rng(topk)
+    lens = [2300, 40, 180]
+    c = Caches(lens, 6, cli=1)
+    rows = [(0, 2299), (0, 2200), (-1, -1), (1, 0), (1, 39), (2, 100), (2, 101), (-1, 5), (0, 64), (0, 2047), (0, 2048)]
+    lists = _random_lists(rows, topk, rng, full)
+    lists[4] = []                                         # a row with nothing selected
+    cfg = lsa.LsaConfig(index_topk=topk, index_init_tokens=1, index_local_tokens=2, cli_factor=1)
+    _mla_case(c, rows, lists, cfg)
+    _mla_case(c, rows, lists, cfg, ws=None)
+
+
+@gpu
+def test_mla_dense_beyond_the_selection_size():
+    # idx NULL over more keys than index_topk (several frames of the softmax), one and many rows
+    c = Caches([5000], 8, cli=1)
+    cfg = lsa.LsaConfig(index_topk=64, index_init_tokens=1, index_local_tokens=2, cli_factor=1)
+    _mla_case(c, [(0, 4999)], None, cfg)
+    _mla_case(c, [(0, 4999)], None, cfg, ws=None)
+    _mla_case(c, [(0, 4999), (0, 3), (0, 2500)], None, cfg)
+
+
+@gpu
+def test_mla_many_rows_walk_every_cta():
+    # more rows than the GPU has SMs, two sub-blocks: CTAs take several rows each
+    rng = np.random.default_rng(3)
+    c = Caches([260, 333], 9, cli=2)
+    rows = [(i % 2, 259 - i // 2 if i % 2 == 0 else 332 - i // 2) for i in range(400)]
+    rows[17] = rows[18] = (-1, -1)
+    cfg = lsa.LsaConfig(index_topk=200, index_init_tokens=1, index_local_tokens=2)
+    lists = _random_lists(rows, 200, rng)
+    lists[33] = []
+    _mla_case(c, rows, lists, cfg)
+
+
+@gpu
+@pytest.mark.parametrize("lat_scale,q_scale", [(2.0 ** -40, 2.0 ** 40), (2.0 ** 30, 2.0 ** -30), (8.0, 4.0), (2.0 ** -30, 1.0)])
+def test_mla_scales_and_peaked_rows(lat_scale, q_scale):
+    # peaked rows: logits of hundreds, the running maximum moves often; and flat ones
+    rng = np.random.default_rng(11)
+    c = Caches([900, 300], 12, cli=1, lat_scale=lat_scale)
+    rows = [(0, 899), (1, 299), (0, 500)]
+    cfg = lsa.LsaConfig(cli_factor=1)
+    _mla_case(c, rows, _random_lists(rows, 2048, rng), cfg, q_scale=q_scale)
+
+
+@gpu
+def test_mla_keys_in_rising_order_of_their_logits():
+    # each later tile beats the maximum so far: every tile rescales what came before
+    c = Caches([1024], 13, cli=1)
+    cfg = lsa.LsaConfig(cli_factor=1)
+    q = _bf16(np.random.default_rng(15).standard_normal((1, 32, 576)) * 3).cuda()
+    x = _vals(q)[0, 0] @ c.lat[0][0].T
+    order = np.argsort(x)
+    for keys in (order, order[::-1]):
+        idx = _i32(np.concatenate([keys, np.full(1024, -1)])[None])
+        out, lse = [torch.empty(1, 32, 512, dtype=torch.bfloat16, device="cuda")], [torch.empty(1, 32, device="cuda")]
+        lsa.fp8_sparse_mla(cfg, None, _i32([1023]), [q], c.latent_pages, c.block_table, idx, _i32([1024]), 1024, out,
+                           lse, None)
+        assert lsa.device_error() == 0
+        want, wl, wt = F.attend(_vals(q)[0], c.lat[0][0], keys, cfg.softmax_scale)
+        tol, ltol = _mla_tol(_vals(q)[0], c.lat[0][0], keys, wt, want, cfg.softmax_scale)
+        assert (np.abs(lse[0][0].double().cpu().numpy() - wl) <= ltol).all()
+        assert (np.abs(_vals(out[0])[0] - want) <= tol).all()
+
+
+@gpu
+def test_mla_repeated_and_bad_indices_and_pages():
+    c = Caches([300, 500], 14, cli=1)
+    cfg = lsa.LsaConfig(index_topk=40, index_init_tokens=1, index_local_tokens=2, cli_factor=1)
+    rows = [(0, 299), (1, 499), (1, 100)]
+    lists = [[5, 5, 5, 64, 299, 0], list(range(100, 140)), [100, 99, 3]]
+    _mla_case(c, rows, lists, cfg)
+    bad = [[5, -1, 300, 64, 2 ** 31 - 1, 299], list(range(100, 140)), [101, 99, -7]]
+    _mla_case(c, rows, bad, cfg, want_err=lsa.DEVERR_INDEX)
+    t = c.table.copy()
+    t[1, 2] = c.n_pages                                   # tokens 128..191 of sequence 1
+    c.block_table = _i32(t)
+    _mla_case(c, rows, lists, cfg, want_err=lsa.DEVERR_PAGE, keep=lambda s, k: not (s == 1 and 128 <= k < 192))
+
+
+@gpu
+def test_mla_bad_counts_sequences_and_positions():
+    c = Caches([300], 14, cli=1)
+    cfg = lsa.LsaConfig(index_topk=40, index_init_tokens=1, index_local_tokens=2, cli_factor=1)
+    q = [_bf16(np.random.default_rng(0).standard_normal((4, 32, 576))).cuda()]
+    idx = _i32(np.tile(np.arange(40), (4, 1)))
+    out, lse = [torch.full((4, 32, 512), 9.0, dtype=torch.bfloat16, device="cuda")], [torch.zeros(4, 32, device="cuda")]
+    lsa.fp8_sparse_mla(cfg, _i32([0, 0, 3, 0]), _i32([299, 299, 5, 5000]), q, c.latent_pages, c.block_table, idx,
+                       _i32([-3, 41, 2, 10]), 300, out, lse, None)
+    assert lsa.device_error() == lsa.DEVERR_COUNT | lsa.DEVERR_SEQ | lsa.DEVERR_POS
+    assert (out[0][0] == 0).all() and torch.isneginf(lse[0][0]).all()      # count -3: no keys
+    assert (out[0][2] == 0).all() and torch.isneginf(lse[0][2]).all()      # unknown sequence
+    want, wl, _ = F.attend(_vals(q[0])[1], c.lat[0][0], range(40), cfg.softmax_scale)
+    assert np.allclose(lse[0][1].cpu().numpy(), wl, atol=1e-4)             # count 41: clamped to 40
+    assert np.isfinite(_vals(out[0])).all()
+
+
+@gpu
+def test_mla_non_finite_keys_stay_where_they_are_selected():
+    c = Caches([200], 15, cli=1)
+    c.latent_pages[0].view(-1, 592).view(torch.float32)[c.slots(0, 200)[77], 144] = float("nan")
+    cfg = lsa.LsaConfig(index_topk=64, index_init_tokens=1, index_local_tokens=2, cli_factor=1)
+    rows = [(0, 199), (0, 199)]
+    lists = [list(range(60)), list(range(70, 100))]
+    ih = np.full((2, 64), -1)
+    for r, l in enumerate(lists):
+        ih[r, :len(l)] = l
+    q = [_bf16(np.random.default_rng(0).standard_normal((2, 32, 576))).cuda()]
+    out, lse = [torch.zeros(2, 32, 512, dtype=torch.bfloat16, device="cuda")], [torch.zeros(2, 32, device="cuda")]
+    lsa.fp8_sparse_mla(cfg, _i32([0, 0]), _i32([199, 199]), q, c.latent_pages, c.block_table, _i32(ih), _i32([60, 30]),
+                       200, out, lse, None)
+    assert lsa.device_error() == 0
+    assert torch.isfinite(out[0][0]).all() and torch.isfinite(lse[0][0]).all()
+    assert torch.isnan(out[0][1]).all() and torch.isnan(lse[0][1]).all()
+
+
+# ------------------------------------------------------------------ GPU: large offsets, streams, graphs
+
+
+@gpu
+def test_offsets_beyond_32_bits():
+    # pools of more than 2^32 bytes, the sequences in their last pages
+    c = Caches([200, 70], 16, cli=1, first_page=115000)
+    cfg = lsa.LsaConfig(index_topk=100, index_init_tokens=1, index_local_tokens=2, cli_factor=1)
+    rows = [(0, 199), (1, 69)]
+    assert c.latent_pages[0].numel() > 2 ** 32
+    _mla_case(c, rows, _random_lists(rows, 100, np.random.default_rng(0)), cfg)
+    x = torch.ones(1, 576, dtype=torch.bfloat16, device="cuda")
+    last = c.n_pages * 64 - 1
+    lsa.fp8_append(cfg, _i32([last]), [x], c.latent_pages)
+    assert int(c.latent_pages[0].view(-1, 592)[last, 0]) == 0x78            # 1 = 2^-8 * 256
+    del c
+    k = Caches([200, 70], 16, cli=0, first_page=510000)
+    assert k.key_pages.numel() > 2 ** 32
+    assert _score_case([200, 70], rows, lsa.LsaConfig(**TINY), caches=k)[0] == 0
+    assert _score_case([200, 70], [(0, p) for p in range(150, 200)], lsa.LsaConfig(**TINY), caches=k)[0] == 0
+
+
+def _layer_inputs(rng, n, cli=2):
+    q_idx = _bf16(rng.standard_normal((n, 32, 128))).cuda()
+    w = torch.from_numpy((rng.standard_normal((n, 32)) / 32 ** 0.5).astype(np.float32)).cuda()
+    q = [_bf16(rng.standard_normal((n, 32, 576))).cuda() for _ in range(cli)]
+    out = [torch.zeros(n, 32, 512, dtype=torch.bfloat16, device="cuda") for _ in range(cli)]
+    lse = [torch.zeros(n, 32, device="cuda") for _ in range(cli)]
+    return q_idx, w, q, out, lse
+
+
+@gpu
+def test_serving_run_from_plan_to_layer():
+    """Requests arrive, are planned, appended in two steps (a prompt chunk, then decode tokens) and attended;
+    the last step runs as a captured graph too, twice, on a side stream."""
+    rng = np.random.default_rng(21)
+    cfg = lsa.LsaConfig(index_topk=96, index_init_tokens=4, index_local_tokens=16)
+    ocfg = R.LsaConfig(index_topk=96, index_init_tokens=4, index_local_tokens=16)
+    n_seq, width, n_pages = 3, 8, 30
+    bt = torch.full((n_seq, width), -1, dtype=torch.int32, device="cuda")
+    lp, kp = [lsa.latent_pages(n_pages) for _ in range(2)], lsa.key_pages(n_pages)
+    free = rng.permutation(n_pages)
+    used = 0
+    cached = np.zeros(n_seq, dtype=np.int64)
+    vals = {"k": [np.zeros((0, 128))] * n_seq, "c0": [np.zeros((0, 576))] * n_seq, "c1": [np.zeros((0, 576))] * n_seq}
+    for step, fresh in enumerate(([150, 64, 1], [1, 1, 1], [200, 1, 0], [1, 1, 1])):
+        fresh = np.array(fresh)
+        cap = int(fresh.sum()) + 2
+        seq, pos, slot, totals = (torch.empty(k, dtype=torch.int32, device="cuda") for k in (cap, cap, cap, 2))
+        lsa.page_plan(_i32(cached), _i32(fresh), _i32(free[used:]), bt, seq, pos, slot, totals)
+        used += int(totals[1])
+        k = _bf16(rng.standard_normal((cap, 128))).cuda()
+        lat = [_bf16(rng.standard_normal((cap, 576))).cuda() for _ in range(2)]
+        lsa.fp8_append(cfg, slot, lat, lp, k, kp)
+        sh, ph = seq.cpu().numpy(), pos.cpu().numpy()
+        for name, x in (("k", k), ("c0", lat[0]), ("c1", lat[1])):
+            d = F.dequant(*F.quant(_vals(x)))
+            vals[name] = [np.concatenate([v, d[sh == s]]) for s, v in enumerate(vals[name])]
+        cached = cached + fresh
+        max_len = int(cached.max())
+        q_idx, w, q, out, lse = _layer_inputs(rng, cap)
+        idx = torch.full((cap, 96), -1, dtype=torch.int32, device="cuda")
+        cnt = torch.zeros(cap, dtype=torch.int32, device="cuda")
+        ws = lsa.workspace(cfg, lsa.OP_FP8_FORWARD, cap, n_seq, max_len)
+
+        def layer():
+            lsa.fp8_forward(cfg, seq, pos, max_len, q_idx, w, kp, q, lp, bt, out, lse, ws, idx_out=idx, count_out=cnt)
+
+        layer()
+        assert lsa.device_error() == 0
+        if step == 3:  # captured and replayed, on another stream
+            eager = [o.clone() for o in out]
+            s2 = torch.cuda.Stream()
+            s2.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s2):
+                layer()
+                g = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(g, stream=s2):
+                    layer()
+                for o in out:
+                    o.zero_()
+                g.replay()
+                g.replay()
+            torch.cuda.current_stream().wait_stream(s2)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(eager, out)) and lsa.device_error() == 0
+            del g
+        ih, ch = idx.cpu().numpy(), cnt.cpu().numpy()
+        for r in range(cap):
+            if sh[r] < 0:
+                assert not out[0][r].any()
+                continue
+            s, p = int(sh[r]), int(ph[r])
+            sel = ih[r, :ch[r]]
+            assert len(set(sel.tolist())) == ch[r] == min(p + 1, 96) and sel.min() >= 0 and sel.max() <= p
+            sc = F.score_row(_vals(q_idx)[r], w.double().cpu().numpy()[r], vals["k"][s], p, ocfg)
+            want_idx, gap = R.select_topk(sc, p, ocfg)
+            if p + 1 > 96 and gap is not None and gap > 1e-4:
+                np.testing.assert_array_equal(np.sort(sel), np.sort(want_idx))
+            for z in range(2):
+                c = vals[f"c{z}"][s]
+                o, l, wt = F.attend(_vals(q[z])[r], c, sel, cfg.softmax_scale)
+                tol, ltol = _mla_tol(_vals(q[z])[r], c, sel, wt, o, cfg.softmax_scale)
+                assert (np.abs(lse[z][r].double().cpu().numpy() - l) <= ltol).all()
+                assert (np.abs(_vals(out[z])[r] - o) <= tol).all()
+
+
+@gpu
+def test_forward_dense_small_workspace_and_split_rows():
+    rng = np.random.default_rng(22)
+    lens = [90, 60]
+    c = Caches(lens, 17, cli=2)
+    cfg = lsa.LsaConfig(index_topk=96, index_init_tokens=4, index_local_tokens=16)
+    q_idx, w, q, out, lse = _layer_inputs(rng, 2)
+    # max_len <= topk: no index pass, no key pages needed
+    lsa.fp8_forward(cfg, None, _i32([89, 59]), 90, None, None, None, q, c.latent_pages, c.block_table, out, lse, None)
+    assert lsa.device_error() == 0
+    for r, n in enumerate(lens):
+        o, l, wt = F.attend(_vals(q[1])[r], c.lat[1][r], range(n), cfg.softmax_scale)
+        tol, _ = _mla_tol(_vals(q[1])[r], c.lat[1][r], range(n), wt, o, cfg.softmax_scale)
+        assert (np.abs(_vals(out[1])[r] - o) <= tol).all()
+    # a workspace of fewer rows than the call has: the same results, block by block, with and without a row map
+    lens = [150, 300, 220, 97, 260]
+    c = Caches(lens, 18, cli=2)
+    q_idx, w, q, out, lse = _layer_inputs(rng, 5)
+    pos, seq = _i32([n - 1 for n in lens]), _i32(range(5))
+    full = lsa.workspace(cfg, lsa.OP_FP8_FORWARD, 5, 5, 300)
+    small = lsa.workspace(cfg, lsa.OP_FP8_FORWARD, 2, 5, 300)
+    assert small.numel() < full.numel()
+    got = []
+    for sq, ws in ((seq, full), (None, full), (seq, small), (None, small)):
+        o = [torch.zeros_like(x) for x in out]
+        ix, cn = torch.zeros(5, 96, dtype=torch.int32, device="cuda"), torch.zeros(5, dtype=torch.int32, device="cuda")
+        lsa.fp8_forward(cfg, sq, pos, 300, q_idx, w, c.key_pages, q, c.latent_pages, c.block_table, o, lse, ws, idx_out=ix,
+                        count_out=cn)
+        assert lsa.device_error() == 0
+        got.append((o, ix.sort(1)[0]))
+    for o, ix in got[1:]:
+        assert torch.equal(ix, got[0][1])
+        for a, b in zip(o, got[0][0]):
+            assert (a.float() - b.float()).abs().max() <= 2.0 ** -6 * b.float().abs().max()
