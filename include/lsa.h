@@ -476,7 +476,9 @@ LSA_API lsa_status lsa_forward(const lsa_config* cfg, int32_t mode, int32_t n_ro
  * codes: it stands for NaN throughout. The cached vector stands for scale * code.
  *
  * Latent pages: uint8 [n_pages, 64, LSA_FP8_LATENT_ROW]: a token's 576 codes,
- *   its fp32 scale at byte 576, then 12 bytes of padding (written as zero).
+ *   its fp32 scale at byte 576, a uint32 at byte 580 (1 when every code is zero,
+ *   else 0: the attention then leaves the row's scale, which is arbitrary, out
+ *   of the range of its weights), and 8 bytes of padding (zero).
  * Key pages: uint8 [n_pages, LSA_FP8_KEY_PAGE]: 64 tokens x 128 codes, then the
  *   64 tokens' fp32 scales at byte 8192.
  * block_table int32 [n_seq, max_pages]: token t of sequence b lives in page
@@ -570,8 +572,9 @@ LSA_API lsa_status lsa_fp8_index_scores(const lsa_config* cfg, int32_t n_rows, i
  * q_abs, latent_pages, out, lse: HOST arrays of n_sub DEVICE pointers (lse, or
  * an entry of it, may be NULL): q_abs bf16 [n_rows, 32, 576], out bf16
  * [n_rows, 32, 512], lse fp32 [n_rows, 32]. The query enters to its last bit
- * (to 2^-22 of its head's largest element); the softmax weights are rounded to
- * 8 significant bits, as a bf16 weight is. Logits, sums and outputs accumulate in fp32.
+ * (to 2^-22 of its head's largest element); the softmax weights times their
+ * scales are rounded to 8 significant bits, as a bf16 weight is, and lost below
+ * 2^-19 of the largest of them. Logits, sums and outputs accumulate in fp32.
  * Workspace optional (split-K partials): lsa_workspace_size(LSA_OP_FP8_MLA).
  */
 LSA_API lsa_status lsa_fp8_sparse_mla(const lsa_config* cfg, int32_t n_sub, int32_t n_rows, int32_t n_seq,

@@ -14,6 +14,34 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
+// Two fp16 -> two e4m3 codes, and back (exact).
+__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t h2) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;\n" : "=h"(r) : "r"(h2));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16_e4m3x2(uint32_t two) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(h) : "h"((uint16_t)two));
+  return h;
+}
+__device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// hi = e4m3(x), lo = e4m3((x - hi) * k) of two fp16 values; k a power of two (the
+// difference is exact in fp16: hi has the value's exponent and fewer bits).
+template <int K>
+__device__ __forceinline__ void split_e4m3(uint32_t h2, uint32_t& hi, uint32_t& lo) {
+  constexpr uint32_t k2 = K == 16 ? 0x4c004c00u : 0x54005400u;  // fp16 16 and 64
+  static_assert(K == 16 || K == 64, "the fp16 constants above");
+  hi = e4m3x2_f16(h2);
+  uint32_t d;
+  asm("{\n .reg .b32 t;\n sub.rn.f16x2 t, %1, %2;\n mul.rn.f16x2 %0, t, %3;\n}\n" : "=r"(d) : "r"(h2), "r"(f16_e4m3x2(hi)), "r"(k2));
+  lo = e4m3x2_f16(d);
+}
+
 // The scale's exponent for a vector whose largest magnitude has these bf16 bits
 // (sign cleared): the smallest e with amax <= 448 * 2^e, 448 = 1.75 * 2^8, at
 // least -126. A zero vector takes e = 0. The caller handles non-finite bits.

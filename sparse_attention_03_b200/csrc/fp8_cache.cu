@@ -143,9 +143,10 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PagePlanArgs a)
 
 // One warp quantises one vector of N bf16 (N a multiple of 8): 16-byte chunks
 // lane, lane + 32, ...; the largest magnitude by a warp reduction on the bit
-// patterns, then one multiply and one conversion per element.
+// patterns, then one multiply and one conversion per element. Returns the scale,
+// and the bits 1 for a vector of zeros.
 template <int N>
-__device__ __forceinline__ float quant_row(const uint16_t* __restrict__ src, uint8_t* dst, int lane) {
+__device__ __forceinline__ float2 quant_row(const uint16_t* __restrict__ src, uint8_t* dst, int lane) {
   constexpr int kChunks = N / 8, kPer = (kChunks + 31) / 32;
   uint4 v[kPer];
   uint32_t m = 0;
@@ -164,7 +165,7 @@ __device__ __forceinline__ float quant_row(const uint16_t* __restrict__ src, uin
     const int c = lane + 32 * i;
     if (c < kChunks) *reinterpret_cast<uint2*>(dst + 8 * c) = fin ? quant8(v[i], inv) : make_uint2(0, 0);
   }
-  return fin ? pow2i(e) : __uint_as_float(0x7fc00000u);
+  return make_float2(fin ? pow2i(e) : __uint_as_float(0x7fc00000u), __uint_as_float(m == 0 ? 1u : 0u));
 }
 
 constexpr int kAppendWarps = 8;
@@ -183,11 +184,11 @@ __global__ void __launch_bounds__(kAppendWarps * 32) fp8_append_kernel(Fp8Append
   }
   if (y < 2) {
     uint8_t* dst = a.dst[y] + (int64_t)slot * kLatRow;
-    const float s = quant_row<kDLat>(a.src[y] + r * a.ld[y], dst, lane);
-    if (lane == 0) *reinterpret_cast<uint4*>(dst + kDLat) = make_uint4(__float_as_uint(s), 0, 0, 0);
+    const float2 s = quant_row<kDLat>(a.src[y] + r * a.ld[y], dst, lane);
+    if (lane == 0) *reinterpret_cast<uint4*>(dst + kDLat) = make_uint4(__float_as_uint(s.x), __float_as_uint(s.y), 0, 0);
   } else {
     uint8_t* page = a.dst[2] + (int64_t)(slot / kPage) * kKeyPage;
-    const float s = quant_row<kDi>(a.src[2] + r * a.ld[2], page + (slot % kPage) * kDi, lane);
+    const float s = quant_row<kDi>(a.src[2] + r * a.ld[2], page + (slot % kPage) * kDi, lane).x;
     if (lane == 0) *reinterpret_cast<float*>(page + kPage * kDi + 4 * (slot % kPage)) = s;
   }
 }

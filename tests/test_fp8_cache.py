@@ -225,7 +225,7 @@ class Caches:
         order = rng.permutation(n_pages) + first_page
         self.n_pages = n_pages + first_page
         self.table = np.full((len(lens), max(per)), -1, dtype=np.int64)
-        self.lens, self.keys, self.lat = lens, [], [[] for _ in range(cli)]
+        self.lens, self.keys, self.lat, self.lat_s = lens, [], [[] for _ in range(cli)], [[] for _ in range(cli)]
         at = 0
         for s, n in enumerate(per):
             self.table[s, :n] = order[at:at + n]
@@ -241,6 +241,7 @@ class Caches:
                 x = rng.standard_normal((n, F.LAT)) * lat_scale * 2.0 ** rng.integers(-3, 2, (n, 1))
                 c, sc = F.quant(_vals(_bf16(x)))
                 self.lat[z].append(F.dequant(c, sc))
+                self.lat_s[z].append(sc)
                 self._put_lat(z, s, c, sc)
         self.block_table = _i32(self.table)
 
@@ -297,17 +298,19 @@ def _score_case(lens, rows, cfg, seed=0, n_seq_of=None, hist=False, max_len=None
     return err, scores, pos, h, c
 
 
-def _mla_tol(q, c_val, keys, weights, out, scale):
+def _mla_tol(q, c_val, s, keys, weights, out, scale):
     """Bounds of the kernel's roundings: the output's bf16 (half a step, 2^-8 relative), the weights' two 4-bit
-    pieces (2^-8), the flush of weights below 2^-19 of the largest, and the logits' fp32 sums of 576 exact
+    pieces (2^-8), the flush of weight * scale below 2^-19 of the largest (it multiplies the codes), and the logits' fp32 sums of 576 exact
     products (a truncated addition loses 2^-23 of the absolute sum) with the query's split (2^-22 of the head's
     largest element): delta, once in a weight and once in the sum."""
     c = c_val[np.asarray(keys)]
     delta = scale * (577 * 2.0 ** -23 * (np.abs(q) @ np.abs(c).T)
                      + 2.0 ** -22 * np.abs(q).max(1)[:, None] * np.abs(c).sum(1)[None]).max(1) + 2.0 ** -18
     v = np.abs(c[:, :512])
+    s = np.asarray(s)[np.asarray(keys)]
+    s_loud = np.where(c.any(axis=1), s, 0.0)             # a row of zeros has an arbitrary scale, which does not count
     tol = 2.0 ** -8 * np.abs(out) + (2.0 ** -8 + 2 * delta[:, None] + 2.0 ** -16) * (weights @ v) \
-        + 2.0 ** -19 * weights.max(1, keepdims=True) * v.sum(0)[None] + 1e-37
+        + 2.0 ** -19 * (weights * s_loud).max(1, keepdims=True) * (v / s[:, None]).sum(0)[None] + 1e-37
     return tol, delta + 2.0 ** -18
 
 
@@ -343,7 +346,7 @@ def _mla_case(c, rows, lists, cfg, seed=0, topk=None, q_scale=1.0, identity=Fals
                 assert (o[r] == 0).all() and np.isneginf(l[r]).all()
                 continue
             want, wl, wt = F.attend(qv[r], c.lat[z][s], keys, cfg.softmax_scale)
-            tol, ltol = _mla_tol(qv[r], c.lat[z][s], keys, wt, want, cfg.softmax_scale)
+            tol, ltol = _mla_tol(qv[r], c.lat[z][s], c.lat_s[z][s], keys, wt, want, cfg.softmax_scale)
             assert (np.abs(l[r] - wl) <= ltol).all(), (z, r, np.abs(l[r] - wl).max())
             assert (np.abs(o[r] - want) <= tol).all(), (z, r, (np.abs(o[r] - want) / tol).max())
     return out, lse
@@ -457,6 +460,7 @@ def test_append_codes_and_scales_bit_for_bit(n, n_sub, gap, keys):
         want[slot[live], :576] = c[live]
         want[slot[live], 576:580] = s.astype(np.float32)[live, None].view(np.uint8)
         want[slot[live], 580:] = 0
+        want[slot[live], 580] = (lat[z][1][live] == 0).all(axis=1)
         got = lp[z].view(-1, 592).cpu().numpy().copy()
         nan = np.isnan(s) & live
         assert np.isnan(got[slot[nan], 576:580].copy().view(np.float32)).all()
@@ -682,9 +686,37 @@ def test_mla_keys_in_rising_order_of_their_logits():
                            lse, None)
         assert lsa.device_error() == 0
         want, wl, wt = F.attend(_vals(q)[0], c.lat[0][0], keys, cfg.softmax_scale)
-        tol, ltol = _mla_tol(_vals(q)[0], c.lat[0][0], keys, wt, want, cfg.softmax_scale)
+        tol, ltol = _mla_tol(_vals(q)[0], c.lat[0][0], c.lat_s[0][0], keys, wt, want, cfg.softmax_scale)
         assert (np.abs(lse[0][0].double().cpu().numpy() - wl) <= ltol).all()
         assert (np.abs(_vals(out[0])[0] - want) <= tol).all()
+
+
+@gpu
+def test_mla_a_row_of_zeros_takes_weight_but_no_precision():
+    # a zero key holds most of the softmax; the others' small weights keep their 8 bits
+    rng = np.random.default_rng(30)
+    lat = _bf16(np.concatenate([np.zeros((1, 576)), rng.standard_normal((700, 576)) * 0.01])).cuda()
+    c = Caches([701], 31, cli=1)
+    t = torch.arange(701, device="cuda")
+    slot = (torch.from_numpy(c.table[0]).cuda()[t // 64] * 64 + t % 64).int()
+    cfg = lsa.LsaConfig(cli_factor=1)
+    # every other key's logit is near -9 (in nats): q is opposed to the keys' common direction
+    lat2 = _vals(lat)
+    lat2[1:] += 0.3
+    lat2 = _bf16(lat2).cuda()
+    lat2[0] = 0
+    lsa.fp8_append(cfg, slot, [lat2], c.latent_pages)
+    codes, s = F.quant(_vals(lat2))
+    c.lat[0][0], c.lat_s[0][0] = F.dequant(codes, s), s
+    qq = _bf16(np.broadcast_to(-0.72 + 0.05 * rng.standard_normal((1, 32, 576)), (1, 32, 576))).cuda()
+    out, lse = [torch.empty(1, 32, 512, dtype=torch.bfloat16, device="cuda")], [torch.empty(1, 32, device="cuda")]
+    lsa.fp8_sparse_mla(cfg, None, _i32([700]), [qq], c.latent_pages, c.block_table, None, None, 701, out, lse, None)
+    assert lsa.device_error() == 0
+    want, wl, wt = F.attend(_vals(qq)[0], c.lat[0][0], range(701), cfg.softmax_scale)
+    assert wt[:, 0].min() > 0.5 and wt[:, 1:].max() < 2.0 ** -10
+    tol, ltol = _mla_tol(_vals(qq)[0], c.lat[0][0], s, range(701), wt, want, cfg.softmax_scale)
+    assert (np.abs(lse[0][0].double().cpu().numpy() - wl) <= ltol).all()
+    assert (np.abs(_vals(out[0])[0] - want) <= tol).all()
 
 
 @gpu
@@ -782,7 +814,8 @@ def test_serving_run_from_plan_to_layer():
     free = rng.permutation(n_pages)
     used = 0
     cached = np.zeros(n_seq, dtype=np.int64)
-    vals = {"k": [np.zeros((0, 128))] * n_seq, "c0": [np.zeros((0, 576))] * n_seq, "c1": [np.zeros((0, 576))] * n_seq}
+    vals = {"k": [np.zeros((0, 128))] * n_seq, "c0": [np.zeros((0, 576))] * n_seq, "c1": [np.zeros((0, 576))] * n_seq,
+            "s0": [np.zeros(0)] * n_seq, "s1": [np.zeros(0)] * n_seq}
     for step, fresh in enumerate(([150, 64, 1], [1, 1, 1], [200, 1, 0], [1, 1, 1])):
         fresh = np.array(fresh)
         cap = int(fresh.sum()) + 2
@@ -794,8 +827,11 @@ def test_serving_run_from_plan_to_layer():
         lsa.fp8_append(cfg, slot, lat, lp, k, kp)
         sh, ph = seq.cpu().numpy(), pos.cpu().numpy()
         for name, x in (("k", k), ("c0", lat[0]), ("c1", lat[1])):
-            d = F.dequant(*F.quant(_vals(x)))
+            codes, sc = F.quant(_vals(x))
+            d = F.dequant(codes, sc)
             vals[name] = [np.concatenate([v, d[sh == s]]) for s, v in enumerate(vals[name])]
+            if name != "k":
+                vals["s" + name[1]] = [np.concatenate([v, sc[sh == s]]) for s, v in enumerate(vals["s" + name[1]])]
         cached = cached + fresh
         max_len = int(cached.max())
         q_idx, w, q, out, lse = _layer_inputs(rng, cap)
@@ -838,9 +874,9 @@ def test_serving_run_from_plan_to_layer():
             if p + 1 > 96 and gap is not None and gap > 1e-4:
                 np.testing.assert_array_equal(np.sort(sel), np.sort(want_idx))
             for z in range(2):
-                c = vals[f"c{z}"][s]
+                c, cs = vals[f"c{z}"][s], vals[f"s{z}"][s]
                 o, l, wt = F.attend(_vals(q[z])[r], c, sel, cfg.softmax_scale)
-                tol, ltol = _mla_tol(_vals(q[z])[r], c, sel, wt, o, cfg.softmax_scale)
+                tol, ltol = _mla_tol(_vals(q[z])[r], c, cs, sel, wt, o, cfg.softmax_scale)
                 assert (np.abs(lse[z][r].double().cpu().numpy() - l) <= ltol).all()
                 assert (np.abs(_vals(out[z])[r] - o) <= tol).all()
 
@@ -857,7 +893,7 @@ def test_forward_dense_small_workspace_and_split_rows():
     assert lsa.device_error() == 0
     for r, n in enumerate(lens):
         o, l, wt = F.attend(_vals(q[1])[r], c.lat[1][r], range(n), cfg.softmax_scale)
-        tol, _ = _mla_tol(_vals(q[1])[r], c.lat[1][r], range(n), wt, o, cfg.softmax_scale)
+        tol, _ = _mla_tol(_vals(q[1])[r], c.lat[1][r], c.lat_s[1][r], range(n), wt, o, cfg.softmax_scale)
         assert (np.abs(_vals(out[1])[r] - o) <= tol).all()
     # a workspace of fewer rows than the call has: the same results, block by block, with and without a row map
     lens = [150, 300, 220, 97, 260]
