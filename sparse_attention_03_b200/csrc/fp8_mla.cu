@@ -15,9 +15,9 @@
 //   - the query, scaled per head by a power of two to at most 448, k = 16: bf16
 //     has 8 significant bits, two e4m3 of 4 bits hold them exactly down to 2^-22
 //     of the head's largest element;
-//   - the weight u = p * s_i * 2^(4 - A), at most 128, k = 64: 8 significant
-//     bits, the precision of a bf16 weight; what lies below 2^-20 of the largest
-//     u of its frame is lost.
+//   - the weight u = p * s_i * 2^(2 - A), at most 128, k = 64: 8 significant
+//     bits, the precision of a bf16 weight, in steps of at least 2^-15 (2^-16 of
+//     the largest u of its frame: what is below is lost).
 // The frame A of each head (an integer, so that rescaling is exact) follows the
 // running maximum of log2(p s): it is set from the first tile, raised when a u
 // would pass 128, and set anew every 16 tiles (also downwards: O is then scaled
@@ -33,12 +33,13 @@
 // (rows = keys) and MN-major for O (rows = the contraction). Tensor memory: S
 // twice 64 columns, O 4 x 64.
 //
-// Roles (11 warps, one CTA per SM, persistent over (row, sub-block, split)
-// items): 4 softmax warps (a thread = a key of the tile), 4 epilogue warps (Q
-// codes of the next item, then O of this one), 2 gather warps (16-byte cp.async
-// into the swizzled layout, a ring of two tiles), one MMA thread that issues
-// S(t + 1) before O(t), so that the softmax of a tile runs under the products of
-// its neighbours. Every wait is bounded.
+// Roles (16 warps, one CTA per SM, persistent over (row, sub-block, split)
+// items): 8 softmax warps (a thread = a key of the tile and 16 heads), 7 gather warps (16-byte
+// cp.async into the swizzled layout, a ring of two tiles that is refilled chunk
+// by chunk; between tiles the next item's query codes and, the first four, an
+// item's O when its last product is complete), and one MMA warp
+// that issues what is ready, so that the softmax of a tile runs under the
+// products of its neighbours. Every wait is bounded.
 #include "fp8.cuh"
 #include "launch.h"
 #include "tc.cuh"
@@ -52,9 +53,11 @@ constexpr uint32_t kChunkBytes = kTile * 128;    // 16 KB
 constexpr uint32_t kStageBytes = kChunks * kChunkBytes;
 constexpr uint32_t kQChunkBytes = 64 * 128;
 constexpr uint32_t kPBytes = kTile * 64;
-constexpr int kGatherWarps = 2;
-constexpr int kMmaWarp = 8 + kGatherWarps;
-constexpr int kThreads = (kMmaWarp + 1) * 32;     // 11 warps: 168 registers a thread (12 would be allocated alike)
+constexpr int kSoftWarps = 8;                    // two groups of four: heads 0..15 and 16..31
+constexpr int kGatherWarps = 7;                  // the first four also write O
+constexpr int kMmaWarp = kSoftWarps + kGatherWarps;
+constexpr int kThreads = (kMmaWarp + 1) * 32;    // 16 warps, 128 registers a thread
+constexpr int kHG = kH / 2;                      // heads of a softmax group
 constexpr int kFrameTiles = 16;                  // tiles after which the frame is set anew
 constexpr int kMaxSplits = 32;
 constexpr uint32_t kTmemO = 128;                 // S: columns 0..127, O: 128..383
@@ -66,14 +69,17 @@ struct __align__(1024) Fp8MlaSmem {
   uint8_t k[2][kStageBytes];
   uint8_t q[kChunks * kQChunkBytes];   // [chunk][32 hi rows, 32 lo rows][128 B]
   uint8_t p[2][kPBytes];               // [key][32 hi, 32 lo codes]
-  float4 frame[4][kH];                 // per softmax warp: q factor, m, 2^(4 - A + m), A - m + 3
-  float4 move[4][kH];                  // per softmax warp: factors of L and O, shift of x
-  float2 tmax[4][kH];                  // event: each warp's maxima
-  float lsum[4][kH];
+  float4 frame[kSoftWarps][kHG];       // per softmax warp: q factor, -m, 2^(2 - A + m)
+  float2 move[kSoftWarps][kHG];        // per softmax warp: factors of L and O
+  float2 tmax[kSoftWarps][kHG];        // each warp's maxima of a tile
+  float lsum[kSoftWarps][kHG];
   float qf[4][kH];                     // ring over items: the heads' query factors
-  float2 fin[4][kH];                   // ring over items: factor of O, lse (one split) ; 2^(A-m-4), L
+  float2 fin[4][kH];                   // ring over items: 2^(A - m - 2), the sum of the softmax
   float fin_m[4][kH];
-  uint64_t full[2], pv_done[2], s_full[2], s_empty[2], p_full[2], q_full[4], fin_full[4], q_empty, o_full, o_empty, drain;
+  // per stage and chunk: gathered; read by its products (chunk 4, which has none: s_empty)
+  uint64_t full[2][kChunks], pv_done[2][4];
+  uint64_t s_full[2], s_empty[2], p_full[2], q_full[4], fin_full[4], q_empty, o_full, o_empty, drain;
+  int item_tiles[4];                   // ring over items, of the MMA warp
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -86,31 +92,29 @@ struct Split {
 
 // One (row, sub-block, split): its list and its tiles [t0, t1).
 struct Item {
-  int r, z, s, t0, t1;
-  int64_t n, nvis;       // list length, visible keys
-  const int32_t* table;  // the sequence's block-table row
-  bool pad;
+  int r, z, t0, t1;
+  uint32_t n, nvis;  // list length, visible keys
+  int seq;           // -1: no keys
+  bool pad;          // a padding row: nothing of it is written
 };
 
+__device__ __forceinline__ int item_row(const Fp8MlaArgs& a, const Split& sp, int i) { return i / (sp.n_split * a.n_sub); }
+__device__ __forceinline__ int item_sub(const Fp8MlaArgs& a, const Split& sp, int i) { return (i / sp.n_split) % a.n_sub; }
+
 __device__ __forceinline__ Item load_item(const Fp8MlaArgs& a, const Split& sp, int i, bool report) {
-  Item it;
-  it.pad = true;
-  it.t0 = it.t1 = 0;
-  it.r = it.z = it.s = 0;
-  it.n = it.nvis = 0;
-  it.table = nullptr;
+  Item it = {0, 0, 0, 0, 0u, 0u, -1, true};
   if (i >= sp.n_items) return it;
-  it.s = i % sp.n_split;
-  it.z = (i / sp.n_split) % a.n_sub;
-  it.r = i / (sp.n_split * a.n_sub);
-  report = report && it.s == 0 && it.z == 0;
+  const int s = i % sp.n_split;
+  it.z = item_sub(a, sp, i);
+  it.r = item_row(a, sp, i);
+  report = report && s == 0 && it.z == 0;
   const int32_t cnt = a.idx ? a.count[it.r] : 0;
   const PagedGeom g = paged_geom(a.rows, it.r, report);
   it.pad = g.pad;
-  it.nvis = g.nvis;
-  it.n = g.nvis;
+  it.seq = g.seq;
+  it.nvis = (uint32_t)g.nvis;
+  it.n = it.nvis;
   if (g.seq < 0) return it;
-  it.table = a.rows.block_table + (int64_t)g.seq * a.rows.max_pages;
   if (a.idx) {
     it.n = cnt;
     if (cnt < 0 || cnt > a.topk) {
@@ -118,24 +122,30 @@ __device__ __forceinline__ Item load_item(const Fp8MlaArgs& a, const Split& sp, 
       it.n = cnt < 0 ? 0 : a.topk;
     }
   }
-  const int64_t tiles = (it.n + kTile - 1) / kTile;
-  it.t0 = (int)(tiles * it.s / sp.n_split);
-  it.t1 = (int)(tiles * (it.s + 1) / sp.n_split);
+  const uint64_t tiles = ((uint64_t)it.n + kTile - 1) / kTile;
+  it.t0 = (int)(tiles * s / sp.n_split);
+  it.t1 = (int)(tiles * (s + 1) / sp.n_split);
   return it;
 }
 
-// Lane h gets the maximum (or sum) over the warp of v[h]: a butterfly that halves the array.
+// The item's place among the partial outputs.
+__device__ __forceinline__ int64_t item_base(const Fp8MlaArgs& a, const Split& sp, int i) {
+  return ((int64_t)item_sub(a, sp, i) * a.rows.n_rows + item_row(a, sp, i)) * sp.n_split + i % sp.n_split;
+}
+
+// Lanes h and h + 16 get the maximum (or sum) over the warp of v[h]: a butterfly that halves the array.
 template <bool MAX>
-__device__ __forceinline__ float fold32(float (&v)[32], int lane) {
+__device__ __forceinline__ float fold16(float (&v)[kHG], int lane) {
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1)
+  for (int o = 8; o >= 1; o >>= 1)
 #pragma unroll
     for (int i = 0; i < o; ++i) {
       const float send = (lane & o) ? v[i] : v[i + o], keep = (lane & o) ? v[i + o] : v[i];
       const float got = __shfl_xor_sync(0xffffffffu, send, o);
       v[i] = MAX ? fmaxf(keep, got) : keep + got;
     }
-  return v[0];
+  const float got = __shfl_xor_sync(0xffffffffu, v[0], 16);
+  return MAX ? fmaxf(v[0], got) : v[0] + got;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -146,348 +156,70 @@ __device__ __forceinline__ float ex2(float x) {
 // 2^d for integer-valued d, 0 below the normal range.
 __device__ __forceinline__ float pow2f(float d) { return d < -126.f ? 0.f : pow2i((int)fminf(fmaxf(d, -126.f), 126.f)); }
 
-// The softmax warps' barrier with an OR over all of them.
-__device__ __forceinline__ bool softmax_any(bool v) {
+// A softmax group's barrier (1 or 2) with an OR over its threads.
+__device__ __forceinline__ bool softmax_any(int group, bool v) {
   uint32_t r;
   __syncwarp();
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 q, %1, 0;\n bar.red.or.pred p, 1, 128, q;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(r)
-      : "r"((uint32_t)v)
-      : "memory");
+  if (group == 0)
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 q, %1, 0;\n bar.red.or.pred p, 1, 128, q;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(r)
+        : "r"((uint32_t)v)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 q, %1, 0;\n bar.red.or.pred p, 2, 128, q;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(r)
+        : "r"((uint32_t)v)
+        : "memory");
   return r != 0;
 }
 
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_u32(bar)) : "memory");
+// ---------------------------------------------------------------- query codes
+
+// Gather warp w quantises heads w, w + 7, .. of an item's query, once the
+// previous item's last S is complete. A loop over the heads, the next one's
+// loads in flight: the code runs once an item, so that its size counts.
+__device__ __forceinline__ void load_head(const uint4* src, int h, int lane, uint4 (&v)[3]) {
+#pragma unroll
+  for (int c = 0; c < 3; ++c)
+    v[c] = h < kH && lane + 32 * c < 72 ? __ldg(src + h * 72 + lane + 32 * c) : make_uint4(0, 0, 0, 0);
 }
 
-// ---------------------------------------------------------------- gather warps
-
-__device__ __forceinline__ void gather_role(const Fp8MlaArgs& a, const Split& sp, Fp8MlaSmem& sm, int warp, int lane,
-                                            volatile int* abort_flag) {
-  const int key_t = warp * 64 + lane;  // this lane looks up the rows of tile keys key_t and key_t + 32
-  uint32_t g = 0;
-  for (int i = blockIdx.x; i < sp.n_items; i += gridDim.x) {
-    const Item it = load_item(a, sp, i, warp == 0 && lane == 0);
-    const int32_t* list = a.idx ? a.idx + (int64_t)it.r * a.topk : nullptr;
-    const uint8_t* lat = a.lat[it.z];
-    // Row of list entry e: its address, or null when it is masked.
-    auto lookup = [&](int64_t e) -> const uint8_t* {
-      if (e >= it.n) return nullptr;
-      const int64_t key = list ? list[e] : e;
-      if (key < 0 || key >= it.nvis) {
-        flag_error(a.rows.err, LSA_DEVERR_INDEX);
-        return nullptr;
-      }
-      const int page = it.table[key / kPage];
-      if (!page_ok(page, a.rows.n_pages)) {
-        flag_error(a.rows.err, LSA_DEVERR_PAGE);
-        return nullptr;
-      }
-      return lat + ((int64_t)page * kPage + key % kPage) * kLatRow;
-    };
-    const uint8_t *row0 = nullptr, *row1 = nullptr;
-    if (it.t0 < it.t1) {
-      row0 = lookup((int64_t)it.t0 * kTile + key_t);
-      row1 = lookup((int64_t)it.t0 * kTile + key_t + 32);
-    }
-    for (int t = it.t0; t < it.t1; ++t, ++g) {
-      const int b = g & 1;
-      const uint8_t *next0 = nullptr, *next1 = nullptr;
-      if (t + 1 < it.t1) {
-        next0 = lookup((int64_t)(t + 1) * kTile + key_t);
-        next1 = lookup((int64_t)(t + 1) * kTile + key_t + 32);
-      }
-      if (g >= 2 && !mbar_wait(&sm.pv_done[b], ((g >> 1) - 1) & 1, abort_flag)) return;
-      __syncwarp();
-      const uint32_t stage = smem_u32(sm.k[b]);
-      const int unit = lane & 7;
-#pragma unroll
-      for (int q = 0; q < 16; ++q) {  // four keys at a time, eight lanes a key
-        const int k = 4 * q + (lane >> 3);
-        const uint8_t* src = reinterpret_cast<const uint8_t*>(
-            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(q < 8 ? row0 : row1), k & 31));
-        const int bytes = src ? 16 : 0;  // a masked key is all zeros, its scale too
-        const uint8_t* from = (src ? src : lat) + unit * 16;
-        const uint32_t dst = stage + (warp * 64 + k) * 128 + ((unit ^ (k & 7)) << 4);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) cp_async16(dst + c * kChunkBytes, from + c * 128, bytes);
-        if (unit < 5) cp_async16(dst + 4 * kChunkBytes, from + 4 * 128, bytes);
-      }
-      cp_async_arrive(&sm.full[b]);
-      row0 = next0;
-      row1 = next1;
-    }
-  }
-}
-
-// ---------------------------------------------------------------- MMA thread
-
-struct MmaRole {
-  Fp8MlaSmem& sm;
-  uint32_t tmem;
-  volatile int* abort_flag;
-  uint32_t k_addr, q_addr, p_addr;
-
-  __device__ __forceinline__ bool s_tile(uint32_t g, bool last) {
-    const int b = g & 1;
-    if (!mbar_wait(&sm.full[b], (g >> 1) & 1, abort_flag)) return false;
-    if (g >= 2 && !mbar_wait(&sm.s_empty[b], ((g >> 1) - 1) & 1, abort_flag)) return false;
-    fence_proxy_async();  // the tile came through cp.async (generic proxy)
-    tc_fence_after();
-    const uint64_t ad = sw128_desc(k_addr + b * kStageBytes), bd = sw128_desc(q_addr);
-    constexpr uint32_t id = f8_idesc(64, false);
-#pragma unroll
-    for (int ks = 0; ks < 18; ++ks) {
-      const uint32_t c = ks >> 2, o = (ks & 3) * 32;
-      umma_f8(tmem + b * 64, ad + ((c * kChunkBytes + o) >> 4), bd + ((c * kQChunkBytes + o) >> 4), id, ks > 0 ? 1u : 0u);
-    }
-    umma_commit(&sm.s_full[b]);
-    if (last) umma_commit(&sm.q_empty);
-    return true;
-  }
-  __device__ __forceinline__ bool pv_tile(uint32_t g, bool first, bool last, uint32_t nk) {
-    const int b = g & 1;
-    if (!mbar_wait(&sm.p_full[b], (g >> 1) & 1, abort_flag)) return false;
-    if (first && nk > 0 && !mbar_wait(&sm.o_empty, (nk - 1) & 1, abort_flag)) return false;
-    tc_fence_after();
-    const uint64_t ad = sw128_mn_desc(k_addr + b * kStageBytes, 1024), bd = sw64_mn_desc(p_addr + b * kPBytes);
-    constexpr uint32_t id = f8_idesc(64, true);
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        umma_f8(tmem + kTmemO + c * 64, ad + ((c * kChunkBytes + ks * 4096) >> 4), bd + ((ks * 2048) >> 4), id,
-                !first || ks > 0 ? 1u : 0u);
-    umma_commit(&sm.pv_done[b]);
-    if (last) umma_commit(&sm.o_full);
-    return true;
-  }
-};
-
-__device__ __forceinline__ void mma_role(const Fp8MlaArgs& a, const Split& sp, Fp8MlaSmem& sm, uint32_t tmem,
-                                         volatile int* abort_flag) {
-  MmaRole m{sm, tmem, abort_flag, smem_u32(sm.k[0]), smem_u32(sm.q), smem_u32(sm.p[0])};
-  uint32_t g = 0, nk = 0;
-  bool pending = false, p_first = false, p_last = false;
-  uint32_t p_nk = 0;
-  Item nxt = load_item(a, sp, blockIdx.x, false);
-  for (int i = blockIdx.x; i < sp.n_items; i += gridDim.x) {
-    const Item it = nxt;
-    nxt = load_item(a, sp, i + gridDim.x, false);
-    if (it.t0 >= it.t1) continue;
-    for (int t = it.t0; t < it.t1; ++t, ++g) {
-      const bool first = t == it.t0, last = t + 1 == it.t1;
-      if (first) {  // the previous item's last product does not wait for this item's query
-        if (pending && !m.pv_tile(g - 1, p_first, p_last, p_nk)) return;
-        pending = false;
-        if (!mbar_wait(&sm.q_full[nk & 3], (nk >> 2) & 1, abort_flag)) return;
-      }
-      if (!m.s_tile(g, last)) return;
-      if (pending && !m.pv_tile(g - 1, p_first, p_last, p_nk)) return;
-      pending = true;
-      p_first = first;
-      p_last = last;
-      p_nk = nk;
-    }
-    ++nk;
-  }
-  if (pending) m.pv_tile(g - 1, p_first, p_last, p_nk);
-}
-
-// ---------------------------------------------------------------- softmax warps
-
-__device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& sp, Fp8MlaSmem& sm, uint32_t tmem,
-                                             int warp, int lane, volatile int* abort_flag) {
-  const int key = warp * 32 + lane;
-  const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-  float4* frame = sm.frame[warp];
-  float4* move = sm.move[warp];
-  uint32_t g = 0, nk = 0;
-  Item nxt = load_item(a, sp, blockIdx.x, false);
-  for (int i = blockIdx.x; i < sp.n_items; i += gridDim.x) {
-    const Item it = nxt;
-    nxt = load_item(a, sp, i + gridDim.x, false);
-    if (it.t0 >= it.t1) continue;
-    float L[32];
-#pragma unroll
-    for (int h = 0; h < 32; ++h) L[h] = 0.f;
-    float m_h = 0.f, a_h = kUnset, qf_h = 0.f;  // lane h: head h's frames (every warp the same)
-    bool framed = false;
-    for (int t = it.t0; t < it.t1; ++t, ++g) {
-      const int b = g & 1;
-      bool ok = true;
-      if (t == it.t0) {
-        ok = mbar_wait(&sm.q_full[nk & 3], (nk >> 2) & 1, abort_flag);
-        qf_h = sm.qf[nk & 3][lane];
-        frame[lane] = make_float4(qf_h, 0.f, 0.f, 0.f);
-      }
-      ok = ok && mbar_wait(&sm.s_full[b], (g >> 1) & 1, abort_flag);
-      ok = ok && mbar_wait(&sm.full[b], (g >> 1) & 1, abort_flag);  // complete already: this thread reads the tile too
-      if (ok && g >= 2) ok = mbar_wait(&sm.pv_done[b], ((g >> 1) - 1) & 1, abort_flag);  // P's buffer
-      __syncwarp();
-      tc_fence_after();
-      float x[32], lo[32];
-      tmem_ld32_x2(tmem + lanes + b * 64, tmem + lanes + b * 64 + 32, x, lo);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.s_empty[b]);
-      const uint2 tail = *reinterpret_cast<const uint2*>(sm.k[b] + 4 * kChunkBytes + key * 128 + ((4 ^ (key & 7)) << 4));
-      const float s = __uint_as_float(tail.x);
-      const bool valid = s != 0.f;                    // a masked key's row is zeros
-      const bool silent = !valid || tail.y != 0;      // adds nothing to O
-      const float e = (float)((int)(tail.x >> 23) - 127);
-      float over_u = -INFINITY, over_p = -INFINITY;
-#pragma unroll
-      for (int h = 0; h < 32; ++h) {
-        const float4 f = frame[h];
-        x[h] = fmaf(fmaf(lo[h], 0.0625f, x[h]) * f.x, s, -f.y);
-        over_u = fmaxf(over_u, x[h] - f.w);
-        over_p = fmaxf(over_p, x[h]);
-      }
-      if (!valid) {
-#pragma unroll
-        for (int h = 0; h < 32; ++h) x[h] = -INFINITY;
-      }
-      const bool anew = (t - it.t0) % kFrameTiles == 0;
-      const bool need = anew || !framed || !ok || (valid && (over_p > 60.f || (!silent && over_u + e > 0.f)));
-      if (softmax_any(need)) {
-        // Set the frames from this tile's maxima (all four warps, the same values).
-        float v[32];
-#pragma unroll
-        for (int h = 0; h < 32; ++h) v[h] = x[h];
-        const float tl_w = fold32<true>(v, lane);
-#pragma unroll
-        for (int h = 0; h < 32; ++h) v[h] = silent ? -INFINITY : x[h] + e;
-        const float ta_w = fold32<true>(v, lane);
-        sm.tmax[warp][lane] = make_float2(tl_w, ta_w);
-        if (softmax_any(!ok || *abort_flag)) return;
-        float tl = -INFINITY, ta = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          tl = fmaxf(tl, sm.tmax[w][lane].x);
-          ta = fmaxf(ta, sm.tmax[w][lane].y);
-        }
-        const float m_old = m_h, a_old = a_h;
-        if (tl > -INFINITY) m_h = framed ? fmaxf(m_old, ceilf(tl + m_old)) : ceilf(tl + m_old);
-        if (ta > -INFINITY) a_h = fmaxf(ceilf(ta + m_old), anew ? a_old - 60.f : a_old);
-        framed = framed || __any_sync(0xffffffffu, tl > -INFINITY);
-        const float d = a_h - m_h;
-        const float of = pow2f(a_old - a_h);
-        __syncwarp();
-        frame[lane] = make_float4(qf_h, m_h, pow2f(fminf(4.f - d, 126.f)), d + 3.f);
-        move[lane] = make_float4(pow2f(m_old - m_h), of, m_old - m_h, 0.f);
-        __syncwarp();
-#pragma unroll
-        for (int h = 0; h < 32; ++h) {
-          const float4 mv = move[h];
-          L[h] *= mv.x;
-          x[h] += mv.z;
-        }
-        // O so far moves to the new frames, once its last product is complete.
-        if (t > it.t0 && __any_sync(0xffffffffu, of != 1.f)) {
-          mbar_wait(&sm.pv_done[b ^ 1], ((g - 1) >> 1) & 1, abort_flag);
-          __syncwarp();
-          tc_fence_after();
+__device__ __forceinline__ void prepare_q(const Fp8MlaArgs& a, const Split& sp, Fp8MlaSmem& sm, int item, uint32_t nk,
+                                          int warp, int lane) {
+  const uint4* src =
+      reinterpret_cast<const uint4*>(a.q[item_sub(a, sp, item)] + (int64_t)item_row(a, sp, item) * kH * kDLat);
+  uint4 next[3];
+  load_head(src, warp, lane, next);
 #pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
-            float o[32];
-            tmem_ld32(tmem + lanes + kTmemO + c * 32, o);
-#pragma unroll
-            for (int h = 0; h < 32; ++h) o[h] *= move[h].y;
-            tmem_st32(tmem + lanes + kTmemO + c * 32, o);
-          }
-          tc_fence_before();
-        }
-      }
-      // Weights: p for the sum, u = p s 2^(4 - A + m) in two e4m3 pieces for the product.
-      const float su = silent ? 0.f : s;
-      uint32_t hi[8], lw[8];
-#pragma unroll
-      for (int h4 = 0; h4 < 8; ++h4) {
-        float u[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float p = ex2(x[4 * h4 + j]);
-          L[4 * h4 + j] += p;
-          u[j] = p * su * frame[4 * h4 + j].z;
-        }
-        uint32_t h0, h1, l0, l1;
-        split_e4m3<64>(f16x2_rn(u[0], u[1]), h0, l0);
-        split_e4m3<64>(f16x2_rn(u[2], u[3]), h1, l1);
-        hi[h4] = h0 | h1 << 16;
-        lw[h4] = l0 | l1 << 16;
-      }
-      uint8_t* prow = sm.p[b] + key * 64;
-      const int sw = (key >> 1) & 3;
-      *reinterpret_cast<uint4*>(prow + ((0 ^ sw) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      *reinterpret_cast<uint4*>(prow + ((1 ^ sw) << 4)) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-      *reinterpret_cast<uint4*>(prow + ((2 ^ sw) << 4)) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
-      *reinterpret_cast<uint4*>(prow + ((3 ^ sw) << 4)) = make_uint4(lw[4], lw[5], lw[6], lw[7]);
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.p_full[b]);
-    }
-    // The item's sums, for the epilogue.
-    sm.lsum[warp][lane] = fold32<false>(L, lane);
-    if (softmax_any(*abort_flag != 0)) return;
-    if (warp == 0) {
-      const float l = (sm.lsum[0][lane] + sm.lsum[1][lane]) + (sm.lsum[2][lane] + sm.lsum[3][lane]);
-      const int f = nk & 3;
-      const float back = a_h == kUnset ? 0.f : pow2f(a_h - m_h - 4.f);
-      sm.fin[f][lane] = make_float2(back, l);
-      sm.fin_m[f][lane] = m_h;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.fin_full[f]);
-    }
-    ++nk;
-  }
-}
-
-// ---------------------------------------------------------------- epilogue warps
-
-// Quantises heads 8 warp .. 8 warp + 7 of the item's query into the hi and lo rows.
-__device__ __forceinline__ void load_q(const Fp8MlaArgs& a, const Item& it, int warp, int lane, uint4 (&v)[8][3]) {
-  const uint4* src = reinterpret_cast<const uint4*>(a.q[it.z] + (int64_t)it.r * kH * kDLat) + warp * 8 * 72;
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-#pragma unroll
-    for (int c = 0; c < 3; ++c)
-      v[j][c] = lane + 32 * c < 72 ? __ldg(src + j * 72 + lane + 32 * c) : make_uint4(0, 0, 0, 0);
-}
-__device__ __forceinline__ void store_q(const Fp8MlaArgs& a, Fp8MlaSmem& sm, uint32_t nk, int warp, int lane,
-                                        const uint4 (&v)[8][3]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int h = warp * 8 + j;
+  for (int h = warp; h < kH; h += kGatherWarps) {
+    uint4 v[3];
     uint32_t m = 0;
 #pragma unroll
-    for (int c = 0; c < 3; ++c)
-      m = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(m, v[j][c].x), v[j][c].y), v[j][c].z), v[j][c].w);
+    for (int c = 0; c < 3; ++c) {
+      v[c] = next[c];
+      m = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(m, v[c].x), v[c].y), v[c].z), v[c].w);
+    }
+    load_head(src, h + kGatherWarps, lane, next);
     m = fold_max(m);
     const bool fin = bf16_finite(m);
     const int e = fin ? scale_exponent(m) : 0;
-    const float inv = fin ? pow2i(-e) : 0.f;
+    const float inv = pow2i(-e);
 #pragma unroll
     for (int c = 0; c < 3; ++c) {
       const int u = lane + 32 * c;  // eight elements
-      if (u >= 72) break;
-      const uint32_t w[4] = {v[j][c].x, v[j][c].y, v[j][c].z, v[j][c].w};
+      const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
       uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float x0 = fin ? bf16_lo(w[k]) * inv : 0.f, x1 = fin ? bf16_hi(w[k]) * inv : 0.f;
-        hi[k] = e4m3x2(x0, x1);
-        const uint32_t b = f16_e4m3x2(hi[k]);
-        float b0, b1;
-        asm("{\n .reg .f16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}\n" : "=f"(b0), "=f"(b1) : "r"(b));
-        lo[k] = e4m3x2((x0 - b0) * 16.f, (x1 - b1) * 16.f);
-      }
+      for (int k = 0; k < 4; ++k)  // 8 significant bits fit fp16; what is below 2^-24 of the largest goes
+        split_e4m3<16>(fin ? f16x2_rn(bf16_lo(w[k]) * inv, bf16_hi(w[k]) * inv) : 0u, hi[k], lo[k]);
       const int chunk = u >> 4, unit = (u >> 1) & 7, half = (u & 1) * 8;
       uint8_t* base = sm.q + chunk * kQChunkBytes + h * 128 + ((unit ^ (h & 7)) << 4) + half;
-      *reinterpret_cast<uint2*>(base) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-      *reinterpret_cast<uint2*>(base + 32 * 128) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+      if (u < 72) {
+        *reinterpret_cast<uint2*>(base) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+        *reinterpret_cast<uint2*>(base + 32 * 128) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+      }
     }
     if (lane == 0) sm.qf[nk & 3][h] = fin ? pow2i(e) * (a.scale * kLog2e) : __uint_as_float(0x7fc00000u);
   }
@@ -496,86 +228,473 @@ __device__ __forceinline__ void store_q(const Fp8MlaArgs& a, Fp8MlaSmem& sm, uin
   if (lane == 0) mbar_arrive(&sm.q_full[nk & 3]);
 }
 
-__device__ __forceinline__ void epilogue_role(const Fp8MlaArgs& a, const Split& sp, Fp8MlaSmem& sm, uint32_t tmem,
-                                              int warp, int lane, float* part_o, float2* part_ml,
-                                              volatile int* abort_flag) {
-  const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-  uint32_t nk = 0, nq = 0;  // items drained, queries prepared
-  uint4 v[8][3];
-  // The next item with tiles after `i`.
-  auto next_live = [&](int i, Item& it) {
-    for (; i < sp.n_items; i += gridDim.x) {
-      it = load_item(a, sp, i, false);
-      if (it.t0 < it.t1) break;
-    }
-    return i;
-  };
-  Item qi;
-  int qat = next_live(blockIdx.x, qi);
-  if (qat < sp.n_items) {
-    load_q(a, qi, warp, lane, v);
-    store_q(a, sm, nq++, warp, lane, v);
+// ---------------------------------------------------------------- output
+
+// An item whose tiles are all gathered: its last product is tile last_g of the CTA.
+struct Done {
+  int item;  // -1: none
+  uint32_t nk, last_g;
+};
+
+// Writes an item's O once its last product is complete: warp w holds dims w * 32
+// + lane of each 128 (the tensor-memory lanes it may read).
+__device__ __forceinline__ bool write_out(const Fp8MlaArgs& a, const Split& sp, Fp8MlaSmem& sm, uint32_t tmem,
+                                          const Done& done, int warp, int lane, float* part_o, float2* part_ml,
+                                          volatile int* abort_flag) {
+  if (!mbar_wait(&sm.fin_full[done.nk & 3], (done.nk >> 2) & 1, abort_flag)) return false;
+  if (!mbar_wait(&sm.o_full, done.nk & 1, abort_flag)) return false;
+  __syncwarp();
+  tc_fence_after();
+  const int z = item_sub(a, sp, done.item), r = item_row(a, sp, done.item);
+  const int64_t base = item_base(a, sp, done.item);
+  const uint32_t o_addr = tmem + ((uint32_t)(warp * 32) << 16) + kTmemO;
+  const float2 fin = sm.fin[done.nk & 3][lane];  // lane h: head h's factor of O and sum
+  const bool one = sp.n_split == 1;
+  if (warp == 0) {
+    const float m = sm.fin_m[done.nk & 3][lane];
+    if (!one) part_ml[base * kH + lane] = make_float2(m, fin.y);
+    else if (a.lse[z]) a.lse[z][(int64_t)r * kH + lane] = fin.y == 0.f ? -INFINITY : (m + log2f(fin.y)) * kLn2;
   }
+  const float mine = !one ? fin.x : fin.y == 0.f ? 0.f : fin.x / fin.y;
+#pragma unroll 1
+  for (int c = 0; c < 8; ++c) {  // 128 dims, 16 heads at a time (the gather's registers hold a tile)
+    const int h0 = (c & 1) * 16;
+    float o[16], lo[16];
+    tmem_ld16_x2(o_addr + (c >> 1) * 64 + h0, o_addr + (c >> 1) * 64 + 32 + h0, o, lo);
+    if (c == 7) {  // O is read: the next item may start its products
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.o_empty);
+    }
+#pragma unroll
+    for (int h = 0; h < 16; ++h) o[h] = fmaf(lo[h], 0.015625f, o[h]) * __shfl_sync(0xffffffffu, mine, h0 + h);
+    const int d = (c >> 1) * 128 + warp * 32 + lane;
+    if (one) {
+      // neighbouring lanes swap heads, so that each stores two dims of one head
+      uint16_t* og = a.out[z] + ((int64_t)r * kH + h0 + (lane & 1)) * kDV + (d & ~1);
+#pragma unroll
+      for (int h = 0; h < 16; h += 2) {
+        const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? o[h] : o[h + 1], 1);
+        *reinterpret_cast<uint32_t*>(og + h * kDV) = (lane & 1) ? bf16x2_rn(got, o[h + 1]) : bf16x2_rn(o[h], got);
+      }
+    } else {
+      float* po = part_o + (base * kH + h0) * kDV + d;
+#pragma unroll
+      for (int h = 0; h < 16; ++h) po[h * kDV] = o[h];
+    }
+  }
+  return true;
+}
+
+// ---------------------------------------------------------------- gather warps
+
+// The tiles of a CTA's items, one after the other.
+struct TileCursor {
+  Item it;
+  int i, t;  // item, tile in it
+  __device__ __forceinline__ void start(const Fp8MlaArgs& a, const Split& sp, int item, bool report) {
+    for (i = item; i < sp.n_items; i += gridDim.x) {
+      it = load_item(a, sp, i, report);
+      t = it.t0;
+      if (it.t0 < it.t1) return;
+    }
+  }
+  __device__ __forceinline__ void next(const Fp8MlaArgs& a, const Split& sp, bool report) {
+    if (++t >= it.t1) start(a, sp, i + gridDim.x, report);
+  }
+};
+
+// The arrival of this thread's copies so far (it happens when they have landed).
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// A warp takes groups of four keys (eight lanes a key, 16 bytes a lane and
+// copy): groups warp, warp + 7, .. of the tile's 32. The chunks of a tile go one
+// after the other, each into the place that the tile two before has left: the
+// rope and scale chunk when its softmax has read the scales, a value chunk when
+// its own products are complete. The lookups run ahead: the list entries of tile
+// g + 2 and the pages of tile g + 1 are requested while tile g is copied.
+__device__ __forceinline__ void gather_role(const Fp8MlaArgs& a, const Split& sp, Fp8MlaSmem& sm, uint32_t tmem,
+                                            int warp, int lane, float* part_o, float2* part_ml,
+                                            volatile int* abort_flag) {
+  constexpr int kGroups = (kTile / 4 + kGatherWarps - 1) / kGatherWarps;
+  const bool report = warp == 0 && lane == 0;
+  const int unit = lane & 7;
+  // lanes 0 .. 4 kGroups - 1 look up one key each: key lane & 3 of group lane >> 2
+  const int key_t = 4 * (warp + kGatherWarps * (lane >> 2)) + (lane & 3);
+  const bool looks = key_t < kTile && lane < 4 * kGroups;
+  struct Entry {  // this lane's list entry of a tile
+    uint32_t key, nvis;
+    int seq;
+    bool there;
+  };
+  struct Row {  // the page it asks for
+    uint32_t key;
+    int page;
+    bool there;
+  };
+  struct Tag {  // a tile's item (-1: none), whether it is its first and its last
+    int item;
+    bool first, last;
+  };
+  auto entry_of = [&](const TileCursor& c) {
+    Entry e = {(uint32_t)c.t * kTile + key_t, c.it.nvis, c.it.seq, false};
+    e.there = c.i < sp.n_items && looks && e.key < c.it.n;
+    if (e.there && a.idx) e.key = (uint32_t)a.idx[(int64_t)c.it.r * a.topk + e.key];
+    return e;
+  };
+  auto row_of = [&](const Entry& e) {
+    Row r = {e.key, 0, e.there};
+    if (e.there && e.key >= e.nvis) {  // a negative index too
+      flag_error(a.rows.err, LSA_DEVERR_INDEX);
+      r.there = false;
+    }
+    if (r.there) r.page = a.rows.block_table[(int64_t)e.seq * a.rows.max_pages + e.key / kPage];
+    return r;
+  };
+  auto tag_of = [&](const TileCursor& c) {
+    return c.i < sp.n_items ? Tag{c.i, c.t == c.it.t0, c.t + 1 == c.it.t1} : Tag{-1, false, false};
+  };
+  TileCursor ahead;
+  ahead.start(a, sp, blockIdx.x, report);
+  Tag cur = tag_of(ahead);
+  const Entry e0 = entry_of(ahead);
+  if (ahead.i < sp.n_items) ahead.next(a, sp, report);
+  Tag after = tag_of(ahead);
+  Entry entry = entry_of(ahead);  // of the tile after the current one
+  Row row = row_of(e0);
+  Done older = {-1, 0, 0}, newer = {-1, 0, 0};  // items gathered whose O is not written yet
+  uint32_t nk = 0;
+  for (uint32_t g = 0; cur.item >= 0; ++g) {
+    const int b = g & 1;
+    int slot = -1;
+    if (row.there) {
+      if (page_ok(row.page, a.rows.n_pages)) slot = row.page * kPage + (int)(row.key % kPage);
+      else flag_error(a.rows.err, LSA_DEVERR_PAGE);
+    }
+    row = row_of(entry);
+    if (ahead.i < sp.n_items) ahead.next(a, sp, report);
+    entry = entry_of(ahead);
+    int at[kGroups];  // slots of the keys this lane copies 16 bytes of; a masked key is all zeros, its scale too
+#pragma unroll
+    for (int j = 0; j < kGroups; ++j) at[j] = __shfl_sync(0xffffffffu, slot, 4 * j + (lane >> 3));
+    const uint8_t* lat = a.lat[item_sub(a, sp, cur.item)] + unit * 16;
+    const uint32_t stage = smem_u32(sm.k[b]);
+#pragma unroll
+    for (int cc = 0; cc < kChunks; ++cc) {
+      const int c = cc == 0 ? 4 : cc - 1;
+      if (g >= 2 && !mbar_wait(c == 4 ? &sm.s_empty[b] : &sm.pv_done[b][c & 3], ((g >> 1) - 1) & 1, abort_flag)) return;
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < kGroups; ++j) {
+        const int k = 4 * (warp + kGatherWarps * j) + (lane >> 3);
+        if (k < kTile && (c < 4 || unit < 5))
+          cp_async16(stage + c * kChunkBytes + k * 128 + ((unit ^ (k & 7)) << 4),
+                     lat + (int64_t)max(at[j], 0) * kLatRow + c * 128, at[j] >= 0 ? 16 : 0);
+      }
+      cp_async_arrive(&sm.full[b][c]);
+    }
+    if (cur.first) {
+      if (nk > 0 && !mbar_wait(&sm.q_empty, (nk - 1) & 1, abort_flag)) return;
+      __syncwarp();
+      prepare_q(a, sp, sm, cur.item, nk, warp, lane);
+    }
+    // The item that ended two tiles ago is complete (this tile is in its places): its O.
+    if (warp < 4 && older.item >= 0 && older.last_g + 2 == g) {
+      if (!write_out(a, sp, sm, tmem, older, warp, lane, part_o, part_ml, abort_flag)) return;
+      older = newer;
+      newer.item = -1;
+    }
+    if (cur.last) {
+      const Done now = {cur.item, nk++, g};
+      if (older.item < 0) older = now;
+      else newer = now;
+    }
+    cur = after;
+    after = tag_of(ahead);
+  }
+  if (warp >= 4) return;
+#pragma unroll 1
+  while (older.item >= 0) {
+    if (!write_out(a, sp, sm, tmem, older, warp, lane, part_o, part_ml, abort_flag)) return;
+    older = newer;
+    newer.item = -1;
+  }
+}
+
+// ---------------------------------------------------------------- MMA warp
+
+// Output of an item without keys (a split's empty share: its l = 0).
+__device__ __forceinline__ void write_empty(const Fp8MlaArgs& a, const Split& sp, const Item& it, int item, int lane,
+                                            float2* part_ml) {
+  if (sp.n_split > 1) {
+    part_ml[item_base(a, sp, item) * kH + lane] = make_float2(0.f, 0.f);
+    return;
+  }
+  uint4* o = reinterpret_cast<uint4*>(a.out[it.z] + (int64_t)it.r * kH * kDV);
+  for (int j = lane; j < kH * kDV / 8; j += 32) o[j] = make_uint4(0, 0, 0, 0);
+  if (a.lse[it.z]) a.lse[it.z][(int64_t)it.r * kH + lane] = -INFINITY;
+}
+
+// The warp runs together; one lane issues. The two kinds of work, the next S and
+// the products of the last P, are taken as they become ready, O first: it frees the places that the gather waits for.
+__device__ __forceinline__ void mma_role(const Fp8MlaArgs& a, const Split& sp, Fp8MlaSmem& sm, uint32_t tmem,
+                                         int lane, float2* part_ml, volatile int* abort_flag) {
+  const uint32_t k_addr = smem_u32(sm.k[0]), q_addr = smem_u32(sm.q), p_addr = smem_u32(sm.p[0]);
+  const uint32_t leader = elect_one();
+  auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test(bar, parity)) != 0; };
+  // S: tile gs of the CTA, tile ts of ts1 of item ks
+  uint32_t gs = 0, ks = 0;
+  int ts = 0, ts1 = 0, i = blockIdx.x;
+  Item nxt = load_item(a, sp, i, false);
+  // Takes the next item that has tiles; the one after it is requested ahead.
+  auto next_item = [&]() {
+    while (i < sp.n_items) {
+      const Item it = nxt;
+      const int item = i;
+      i += gridDim.x;
+      nxt = load_item(a, sp, i, false);
+      if (it.t0 < it.t1) {
+        ts = 0;
+        ts1 = it.t1 - it.t0;
+        if (lane == 0) sm.item_tiles[ks & 3] = ts1;
+        __syncwarp();
+        return true;
+      }
+      if (!it.pad) write_empty(a, sp, it, item, lane, part_ml);
+    }
+    return false;
+  };
+  bool s_live = next_item();
+  // O: tile gp, tile tp of item kp
+  uint32_t gp = 0, kp = 0;
+  int tp = 0;
+  long long t0 = global_ns();
+  while (s_live || gp < gs) {
+    if (gp < gs) {
+      const int b = gp & 1;
+      if (ready(&sm.p_full[b], (gp >> 1) & 1) && (tp > 0 || kp == 0 || ready(&sm.o_empty, (kp - 1) & 1))) {
+        tc_fence_after();
+        const bool last = tp + 1 == sm.item_tiles[kp & 3];
+        const uint64_t ad = sw128_mn_desc(k_addr + b * kStageBytes, 1024), bd = sw64_mn_desc(p_addr + b * kPBytes);
+        constexpr uint32_t id = f8_idesc(64, true);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_f8(tmem + kTmemO + c * 64, ad + ((c * kChunkBytes + k * 4096) >> 4), bd + ((k * 2048) >> 4), id,
+                    tp > 0 || k > 0 ? 1u : 0u, leader);
+          if (leader) umma_commit(&sm.pv_done[b][c]);
+          __syncwarp();
+        }
+        if (last && leader) umma_commit(&sm.o_full);
+        __syncwarp();
+        ++gp;
+        if (last) {
+          tp = 0;
+          ++kp;
+        } else {
+          ++tp;
+        }
+        t0 = global_ns();
+        continue;
+      }
+    }
+    if (s_live) {
+      const int b = gs & 1;
+      // the last chunk's arrivals come after those of the tile's others
+      if (ready(&sm.full[b][3], (gs >> 1) & 1) && (gs < 2 || ready(&sm.s_empty[b], ((gs >> 1) - 1) & 1)) &&
+          (ts > 0 || ready(&sm.q_full[ks & 3], (ks >> 2) & 1))) {
+        fence_proxy_async();  // the tile came through cp.async (generic proxy)
+        tc_fence_after();
+        const uint64_t ad = sw128_desc(k_addr + b * kStageBytes), bd = sw128_desc(q_addr);
+        constexpr uint32_t id = f8_idesc(64, false);
+#pragma unroll
+        for (int k = 0; k < 18; ++k) {
+          const uint32_t c = k >> 2, o = (k & 3) * 32;
+          umma_f8(tmem + b * 64, ad + ((c * kChunkBytes + o) >> 4), bd + ((c * kQChunkBytes + o) >> 4), id,
+                  k > 0 ? 1u : 0u, leader);
+        }
+        if (leader) {
+          umma_commit(&sm.s_full[b]);
+          if (ts + 1 == ts1) umma_commit(&sm.q_empty);
+        }
+        __syncwarp();
+        ++gs;
+        if (++ts == ts1) {
+          ++ks;
+          s_live = next_item();
+        }
+        t0 = global_ns();
+        continue;
+      }
+    }
+    if (*abort_flag) return;
+    if (global_ns() - t0 > kWaitLimitNs) {
+      *abort_flag = 1;
+      return;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- softmax warps
+
+// The weights of one key (a thread) for the group's 16 heads in the given
+// frames: p for the sum, u = p s 2^(2 - A + m) for the product; S from tensor
+// memory. `su`: the scale, or 0 for a key that adds nothing to O.
+__device__ __forceinline__ void weights(uint32_t s_addr, const float4* frame, bool valid, float s, float su,
+                                        float (&p)[kHG], float (&u)[kHG], float& top_p, float& top_u) {
+  tmem_ld16_x2(s_addr, s_addr + kH, p, u);  // hi and lo
+  top_p = top_u = 0.f;
+#pragma unroll
+  for (int h = 0; h < kHG; ++h) {
+    const float4 f = frame[h];
+    p[h] = ex2(fmaf(fmaf(u[h], 0.0625f, p[h]) * f.x, s, f.y));
+    u[h] = p[h] * (su * f.z);
+    top_p = fmaxf(top_p, p[h]);
+    top_u = fmaxf(top_u, u[h]);
+  }
+  if (!valid) {
+#pragma unroll
+    for (int h = 0; h < kHG; ++h) p[h] = u[h] = 0.f;
+    top_p = top_u = 0.f;
+  }
+}
+
+__device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& sp, Fp8MlaSmem& sm, uint32_t tmem,
+                                             int warp, int lane, volatile int* abort_flag) {
+  const int group = warp >> 2, quarter = warp & 3, w0 = group * 4;
+  const int key = quarter * 32 + lane, h = lane & 15;  // this lane keeps the frames of the group's head h
+  const uint32_t lanes = ((uint32_t)(quarter * 32) << 16) + group * kHG;
+  float4* frame = sm.frame[warp];
+  float2* move = sm.move[warp];
+  uint32_t g = 0, nk = 0;
   for (int i = blockIdx.x; i < sp.n_items; i += gridDim.x) {
     const Item it = load_item(a, sp, i, false);
-    const int64_t base = ((int64_t)it.z * a.rows.n_rows + it.r) * sp.n_split + it.s;
-    if (it.t0 >= it.t1) {  // nothing to attend to
-      if (it.pad) continue;
-      if (sp.n_split > 1) {
-        if (warp == 0) part_ml[base * kH + lane] = make_float2(0.f, 0.f);
-      } else {
-        uint4* o = reinterpret_cast<uint4*>(a.out[it.z] + (int64_t)it.r * kH * kDV) + warp * 512;
-        for (int j = lane; j < 512; j += 32) o[j] = make_uint4(0, 0, 0, 0);
-        if (a.lse[it.z] && warp == 0) a.lse[it.z][(int64_t)it.r * kH + lane] = -INFINITY;
+    const int t0 = it.t0, t1 = it.t1;
+    if (t0 >= t1) continue;
+    float L[kHG];
+#pragma unroll
+    for (int j = 0; j < kHG; ++j) L[j] = 0.f;
+    float m_h = 0.f, a_h = kUnset, qf_h = 0.f;  // head h's frames (every warp of the group the same)
+    bool framed = false;
+    for (int t = t0; t < t1; ++t, ++g) {
+      const int b = g & 1;
+      bool ok = true;
+      if (t == t0) {
+        ok = mbar_wait(&sm.q_full[nk & 3], (nk >> 2) & 1, abort_flag);
+        qf_h = sm.qf[nk & 3][group * kHG + h];
+        frame[h] = make_float4(qf_h, 0.f, 0.f, 0.f);
       }
-      continue;
-    }
-    // the next item's query, as soon as this one's last S is done
-    qat = next_live(i + gridDim.x, qi);
-    if (qat < sp.n_items) load_q(a, qi, warp, lane, v);
-    if (qat < sp.n_items) {
-      if (!mbar_wait(&sm.q_empty, nk & 1, abort_flag)) return;
-      store_q(a, sm, nq++, warp, lane, v);
-    }
-    if (!mbar_wait(&sm.fin_full[nk & 3], (nk >> 2) & 1, abort_flag)) return;
-    if (!mbar_wait(&sm.o_full, nk & 1, abort_flag)) return;
-    __syncwarp();
-    tc_fence_after();
-    const float2* fin = sm.fin[nk & 3];
-    const bool one = sp.n_split == 1;
-    if (warp == 0) {
-      const float l = fin[lane].y, m = sm.fin_m[nk & 3][lane];
-      if (!one) part_ml[base * kH + lane] = make_float2(m, l);
-      else if (a.lse[it.z]) a.lse[it.z][(int64_t)it.r * kH + lane] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-    }
-    float mine = fin[lane].x;  // lane h: the factor of head h
-    if (one) mine = fin[lane].y == 0.f ? 0.f : mine / fin[lane].y;
-#pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-      float o[32], lo[32];
-      tmem_ld32_x2(tmem + lanes + kTmemO + c * 64, tmem + lanes + kTmemO + c * 64 + 32, o, lo);
-      if (c == 3) {  // O is read: the next item may start its products
-        tc_fence_before();
+      ok = ok && mbar_wait(&sm.s_full[b], (g >> 1) & 1, abort_flag);
+      ok = ok && mbar_wait(&sm.full[b][4], (g >> 1) & 1, abort_flag);  // complete already: this thread reads the scales
+      if (ok && g >= 2) ok = mbar_wait(&sm.pv_done[b][3], ((g >> 1) - 1) & 1, abort_flag);  // P's buffer
+      __syncwarp();
+      tc_fence_after();
+      const uint32_t s_addr = tmem + lanes + b * 64;
+      uint2 tail;
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];\n"
+                   : "=r"(tail.x), "=r"(tail.y)
+                   : "r"(smem_u32(sm.k[b] + 4 * kChunkBytes + key * 128 + ((4 ^ (key & 7)) << 4))));
+      const float s = __uint_as_float(tail.x);
+      const bool valid = s != 0.f;                    // a masked key's row is zeros
+      const bool silent = !valid || tail.y != 0;      // adds nothing to O
+      const float su = silent ? 0.f : s;
+      const bool anew = (t - t0) % kFrameTiles == 0;
+      float p[kHG], u[kHG], top_p = 0.f, top_u = 0.f;
+      bool force = anew || !framed || !ok, moved = false;
+      while (true) {
+        if (!force) weights(s_addr, frame, valid, s, su, p, u, top_p, top_u);
+        if (!softmax_any(group, force || (!moved && (top_u > 128.f || top_p > 0x1p60f)))) break;
+        force = false;
+        moved = true;
+        // Set the frames from this tile's maxima (the group's four warps, the same values).
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.o_empty);
-      }
+        tmem_ld16_x2(s_addr, s_addr + kH, p, u);
 #pragma unroll
-      for (int h = 0; h < 32; ++h) o[h] = fmaf(lo[h], 0.015625f, o[h]) * __shfl_sync(0xffffffffu, mine, h);
-      const int d = c * 128 + warp * 32 + lane;
-      if (one) {
-        // neighbouring lanes swap heads, so that each stores two dims of one head
-        uint16_t* og = a.out[it.z] + (int64_t)it.r * kH * kDV + (d & ~1);
-#pragma unroll
-        for (int h = 0; h < 32; h += 2) {
-          const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? o[h] : o[h + 1], 1);
-          const uint32_t two = (lane & 1) ? bf16x2_rn(got, o[h + 1]) : bf16x2_rn(o[h], got);
-          *reinterpret_cast<uint32_t*>(og + (h + (lane & 1)) * kDV) = two;
+        for (int j = 0; j < kHG; ++j) {
+          const float4 f = frame[j];
+          p[j] = valid ? fmaf(fmaf(u[j], 0.0625f, p[j]) * f.x, s, f.y) : -INFINITY;
         }
-      } else {
-        float* po = part_o + base * kH * kDV + d;
+        const float e = (float)((int)(tail.x >> 23) - 127);
 #pragma unroll
-        for (int h = 0; h < 32; ++h) po[h * kDV] = o[h];
+        for (int j = 0; j < kHG; ++j) u[j] = silent ? -INFINITY : p[j] + e;
+        const float tl_w = fold16<true>(p, lane), ta_w = fold16<true>(u, lane);
+        sm.tmax[warp][h] = make_float2(tl_w, ta_w);
+        if (softmax_any(group, !ok || *abort_flag)) return;
+        float tl = -INFINITY, ta = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          tl = fmaxf(tl, sm.tmax[w0 + w][h].x);
+          ta = fmaxf(ta, sm.tmax[w0 + w][h].y);
+        }
+        const float m_old = m_h, a_old = a_h;
+        if (tl > -INFINITY) m_h = framed ? fmaxf(m_old, ceilf(tl + m_old)) : ceilf(tl + m_old);
+        if (ta > -INFINITY) a_h = fmaxf(ceilf(ta + m_old), anew ? a_old - 60.f : a_old);
+        framed = framed || __any_sync(0xffffffffu, tl > -INFINITY);
+        const float of = pow2f(a_old - a_h);
+        __syncwarp();
+        frame[h] = make_float4(qf_h, -m_h, pow2f(fminf(2.f - (a_h - m_h), 126.f)), 0.f);
+        move[h] = make_float2(pow2f(m_old - m_h), of);
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < kHG; ++j) {
+          const float2 mv = move[j];
+          L[j] *= mv.x;
+          u[j] = mv.y;
+        }
+        // O so far moves to the new frames, once its last product is complete.
+        if (t > t0 && __any_sync(0xffffffffu, of != 1.f)) {
+          mbar_wait(&sm.pv_done[b ^ 1][3], ((g - 1) >> 1) & 1, abort_flag);
+          __syncwarp();
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t o = tmem + lanes + kTmemO + c * 64;
+            float lo[kHG];
+            tmem_ld16_x2(o, o + kH, p, lo);
+#pragma unroll
+            for (int j = 0; j < kHG; ++j) {
+              p[j] *= u[j];
+              lo[j] *= u[j];
+            }
+            tmem_st16_x2(o, o + kH, p, lo);
+          }
+        }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.s_empty[b]);  // S and the scales are read
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t h0, h1, l0, l1;
+        split_e4m3<64>(f16x2_rn(u[4 * j], u[4 * j + 1]), h0, l0);
+        split_e4m3<64>(f16x2_rn(u[4 * j + 2], u[4 * j + 3]), h1, l1);
+        hi[j] = h0 | h1 << 16;
+        lo[j] = l0 | l1 << 16;
+      }
+      uint8_t* prow = sm.p[b] + key * 64;
+      const int sw = (key >> 1) & 3;
+      *reinterpret_cast<uint4*>(prow + ((group ^ sw) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(prow + (((2 + group) ^ sw) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.p_full[b]);
+#pragma unroll
+      for (int j = 0; j < kHG; ++j) L[j] += p[j];
+    }
+    // The item's sums, for the output.
+    sm.lsum[warp][h] = fold16<false>(L, lane);
+    if (softmax_any(group, *abort_flag != 0)) return;
+    if (quarter == 0) {
+      const float l = (sm.lsum[w0][h] + sm.lsum[w0 + 1][h]) + (sm.lsum[w0 + 2][h] + sm.lsum[w0 + 3][h]);
+      const int f = nk & 3;
+      sm.fin[f][group * kHG + h] = make_float2(a_h == kUnset ? 0.f : pow2f(a_h - m_h - 2.f), l);
+      sm.fin_m[f][group * kHG + h] = m_h;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.fin_full[f]);
     }
     ++nk;
   }
@@ -593,15 +712,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&sm.full[b], kGatherWarps * 32);
-      mbar_init(&sm.pv_done[b], 1);
+      for (int c = 0; c < kChunks; ++c) mbar_init(&sm.full[b][c], kGatherWarps * 32);
+      for (int c = 0; c < 4; ++c) mbar_init(&sm.pv_done[b][c], 1);
       mbar_init(&sm.s_full[b], 1);
-      mbar_init(&sm.s_empty[b], 4);
-      mbar_init(&sm.p_full[b], 4);
+      mbar_init(&sm.s_empty[b], kSoftWarps);
+      mbar_init(&sm.p_full[b], kSoftWarps);
     }
     for (int b = 0; b < 4; ++b) {
-      mbar_init(&sm.q_full[b], 4);
-      mbar_init(&sm.fin_full[b], 1);
+      mbar_init(&sm.q_full[b], kGatherWarps);
+      mbar_init(&sm.fin_full[b], 2);
     }
     mbar_init(&sm.q_empty, 1);
     mbar_init(&sm.o_full, 1);
@@ -617,16 +736,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort_flag = &sm.abort_flag;
-  if (warp < 4) {
+  // Registers: 512 threads x 128 at launch; the softmax's two warpgroups take 40 a
+  // thread from the other two (2 x 168 + 2 x 88 = 4 x 128).
+  if (warp < kSoftWarps) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;\n" ::);
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n" ::);
+  if (warp < kSoftWarps) {
     softmax_role(a, sp, sm, tmem, warp, lane, abort_flag);
-  } else if (warp < 8) {
-    epilogue_role(a, sp, sm, tmem, warp - 4, lane, part_o, part_ml, abort_flag);
   } else if (warp < kMmaWarp) {
-    gather_role(a, sp, sm, warp - 8, lane, abort_flag);
+    gather_role(a, sp, sm, tmem, warp - kSoftWarps, lane, part_o, part_ml, abort_flag);
     asm volatile("cp.async.wait_all;\n" ::: "memory");  // none in flight when the CTA retires
-  } else if (lane == 0) {
-    mma_role(a, sp, sm, tmem, abort_flag);
-    umma_commit(&sm.drain);  // every product is complete before the tensor memory is freed
+  } else {
+    mma_role(a, sp, sm, tmem, lane, part_ml, abort_flag);
+    __syncwarp();
+    if (elect_one()) umma_commit(&sm.drain);  // every product is complete before the tensor memory is freed
     const long long t0 = global_ns();
     while (!mbar_try_wait(&sm.drain, 0))
       if (global_ns() - t0 > kWaitLimitNs) break;

@@ -300,7 +300,9 @@ def _score_case(lens, rows, cfg, seed=0, n_seq_of=None, hist=False, max_len=None
 
 def _mla_tol(q, c_val, s, keys, weights, out, scale):
     """Bounds of the kernel's roundings: the output's bf16 (half a step, 2^-8 relative), the weights' two 4-bit
-    pieces (2^-8), the flush of weight * scale below 2^-19 of the largest (it multiplies the codes), and the logits' fp32 sums of 576 exact
+    pieces (2^-8), their smallest step (weight * scale is carried as u = hi + lo / 64 with lo an e4m3 of smallest
+    step 2^-9, so u is off by at most 2^-16, and the largest u of a frame is at least 2: 2^-17 of the largest
+    weight * scale, times the codes), and the logits' fp32 sums of 576 exact
     products (a truncated addition loses 2^-23 of the absolute sum) with the query's split (2^-22 of the head's
     largest element): delta, once in a weight and once in the sum."""
     c = c_val[np.asarray(keys)]
@@ -310,7 +312,7 @@ def _mla_tol(q, c_val, s, keys, weights, out, scale):
     s = np.asarray(s)[np.asarray(keys)]
     s_loud = np.where(c.any(axis=1), s, 0.0)             # a row of zeros has an arbitrary scale, which does not count
     tol = 2.0 ** -8 * np.abs(out) + (2.0 ** -8 + 2 * delta[:, None] + 2.0 ** -16) * (weights @ v) \
-        + 2.0 ** -19 * (weights * s_loud).max(1, keepdims=True) * (v / s[:, None]).sum(0)[None] + 1e-37
+        + 2.0 ** -17 * (weights * s_loud).max(1, keepdims=True) * (v / s[:, None]).sum(0)[None] + 1e-37
     return tol, delta + 2.0 ** -18
 
 
