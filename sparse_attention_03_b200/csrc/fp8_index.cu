@@ -1,100 +1,756 @@
 // Lightning indexer over paged 8-bit keys.
+//
 //   score[r, j] = sk[j] * sum_h (w[r,h] * sq[r,h]) * max(0, q8[r,h] . k8[j])
+//
 // (scales are positive, so they leave the ReLU; a scale that is NaN counts as a
-// product of zero, as max(0, NaN) does in the bf16 indexer).
+// product of zero, as max(0, NaN) does in the bf16 indexer). Products of e4m3
+// codes on tcgen05 kind::f8f6f4 with fp32 accumulators: keys as M = 128, heads
+// as N, K = 128 in four instructions. Legacy mma.sync runs e4m3 at less than its
+// bf16 rate here (224 against 351 TFLOP/s, measured) and would hold the
+// streaming form at half of the memory rate.
+//
+// Two kernels. A row of its own (decode) is bound by the key stream: 132 bytes a
+// key against 180 of ~730 cycles a 128-key tile for the products. Rows that
+// share their keys (a prompt's chunk) are bound by the tensor cores and the
+// ReLU-weighted sum over them: 16 rows a CTA, N = 256. The host takes the
+// second form when a sequence has four rows or more on average: there a tile
+// costs ~1100 cycles for up to 16 rows of a sequence, against ~250 (L2) to 730
+// (HBM) for each row of its own.
+//
+// A tile is two pages of 64 keys, each one TMA copy of 8 KB (the 128-byte
+// swizzle) and one bulk copy of its 64 scales into a ring of their own (the
+// epilogue reads them after the tile's stage is free again).
 #include "fp8.cuh"
 #include "launch.h"
+#include "tc.cuh"
 
 namespace lsa {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kKeysPerCta = 256;
+constexpr int kTile = 128;
+constexpr uint32_t kTileBytes = kTile * kDi;  // 16 KB
+constexpr int kScaleRing = 16;                // tiles: more than the stages and accumulators between producer and epilogue
 
-// e4m3 code -> fp32
-__device__ __forceinline__ float2 from_e4m3x2(uint32_t two) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(h) : "h"((uint16_t)two));
-  float lo, hi;
-  asm("{\n .reg .f16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}\n" : "=f"(lo), "=f"(hi) : "r"(h));
-  return make_float2(lo, hi);
+// The scales of a tile's keys, and which of its two pages are there.
+struct __align__(16) TileScales {  // bulk copies land on 16-byte boundaries
+  float s[kTile];
+  int ok[2];
+};
+static_assert(sizeof(TileScales) % 16 == 0 && (kPage * 4) % 16 == 0 && (kPage * kDi) % 16 == 0 && kKeyPage % 16 == 0,
+              "bulk copies: addresses and sizes in 16 bytes");
+
+// One tile's copies, issued by one thread: the pages' codes into `dst` on `full`
+// and their scales into `sc` on `sfull`. page < 0: not in the pool, or past the
+// keys that are visible; nothing is copied for it and what is in its place is
+// never used.
+__device__ __forceinline__ void load_tile(const CUtensorMap* map, const uint8_t* key_pages, int page0, int page1,
+                                          uint8_t* dst, TileScales* sc, uint64_t* full, uint64_t* sfull) {
+  const int n = (page0 >= 0) + (page1 >= 0);
+  sc->ok[0] = page0 >= 0;
+  sc->ok[1] = page1 >= 0;
+  mbar_expect_tx(full, n * kPage * kDi);
+  mbar_expect_tx(sfull, n * kPage * 4);
+  if (page0 >= 0) {
+    tma_load_3d(dst, map, 0, 0, page0, full);
+    bulk_load(sc->s, key_pages + (int64_t)page0 * kKeyPage + kPage * kDi, kPage * 4, sfull);
+  }
+  if (page1 >= 0) {
+    tma_load_3d(dst + kPage * kDi, map, 0, 0, page1, full);
+    bulk_load(sc->s + kPage, key_pages + (int64_t)page1 * kKeyPage + kPage * kDi, kPage * 4, sfull);
+  }
 }
 
-// One CTA: one row, 256 keys; a warp per key in turn, a lane per head.
-__global__ void __launch_bounds__(kThreads) fp8_index_simple_kernel(Fp8IndexArgs a, int row0) {
-  __shared__ float q[kHi][kDi + 1];
-  __shared__ float wq[kHi];
+// A batch of pages looked up by the producer warp, a lane each: pages first ..
+// first + 31 of the sequence (-1: past the visible keys, or outside the pool).
+__device__ __forceinline__ int lookup_pages(const PagedRows& rows, int seq, int64_t nvis, int64_t first, int lane) {
+  const int64_t p = first + lane;
+  if (p * kPage >= nvis) return -1;
+  const int page = rows.block_table[(int64_t)seq * rows.max_pages + p];
+  if (page_ok(page, rows.n_pages)) return page;
+  flag_error(rows.err, LSA_DEVERR_PAGE);
+  return -1;
+}
+
+__device__ __forceinline__ float score_value(float s, float sk) { return sk == sk ? s * sk : 0.f; }
+
+// Quantises one head's 128 query elements over a half warp (8 elements a lane,
+// sub = lane & 15): the codes and the scale (NaN vectors: zeros and 0).
+__device__ __forceinline__ uint2 quant_head(uint4 v, float& scale) {
+  uint32_t m = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(0, v.x), v.y), v.z), v.w);
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, off));
+  m = max(m & 0xffffu, m >> 16);
+  const bool fin = bf16_finite(m);
+  const int e = fin ? scale_exponent(m) : 0;
+  scale = fin ? pow2i(e) : 0.f;
+  return fin ? quant8(v, pow2i(-e)) : make_uint2(0, 0);
+}
+
+// ---------------------------------------------------------------- rows of their own
+
+constexpr int kStages = 8;      // 128 KB of keys in flight
+constexpr int kAcc = 4;         // accumulators of 32 columns
+constexpr int kDecThreads = 10 * 32;
+
+struct RowInfo {
+  int row, seq;
+  int t0, t1;    // its tiles [t0, t1) of this CTA (row -1: no more)
+  int64_t nvis;
+};
+
+struct __align__(1024) DecodeSmem {
+  uint8_t a[kStages][kTileBytes];
+  uint8_t q[2][kHi * kDi];
+  TileScales sc[kScaleRing];
+  float w[2][kHi];
+  RowInfo info[4];
+  unsigned long long sums[kDecThreads];
+  unsigned long long total;
+  int start_row, start_tile;
+  uint64_t full[kStages], empty[kStages], sfull[kScaleRing], tfull[kAcc], tempty[kAcc], qfull[2], qempty[2], rfull[4],
+      rempty[4];
+  uint32_t tmem_base;
+  int abort_flag;
+  uint32_t hist[2048];
+};
+
+__device__ __forceinline__ int64_t row_tiles(const PagedRows& rows, int r, bool report) {
+  return (paged_geom(rows, r, report).nvis + kTile - 1) / kTile;
+}
+
+// The four epilogue warps' barrier with an OR.
+__device__ __forceinline__ bool epilogue_any(bool v) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 q, %1, 0;\n bar.red.or.pred p, 1, 128, q;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+
+// At exit after a wait that gave up: none of this CTA's copies may be in flight
+// into its shared memory. The last tiles' barriers, each with a limit of its own.
+template <int STAGES>
+__device__ __forceinline__ void drain_copies(uint64_t* full, uint64_t* sfull, uint32_t issued) {
+  const long long t0 = global_ns();
+  for (uint32_t i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
+    while (!mbar_try_wait(&full[i % STAGES], (i / STAGES) & 1) ||
+           !mbar_try_wait(&sfull[i % kScaleRing], (i / kScaleRing) & 1))
+      if (global_ns() - t0 > kWaitLimitNs) return;
+}
+
+// Persistent: every CTA sums the rows' tiles and takes an equal share of them
+// (tiles of consecutive rows). Warps: producer, MMA, four for the epilogue (a
+// thread = a key), four for the rows' queries.
+template <bool HIST>
+__global__ void __launch_bounds__(kDecThreads, 1)
+    fp8_index_rows_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ Fp8IndexArgs a) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  if ((smem_u32(smem_raw) & 1023u) != 0) {
+    if (threadIdx.x == 0) flag_error(a.rows.err, LSA_DEVERR_TIMEOUT);
+    return;
+  }
+  DecodeSmem& sm = *reinterpret_cast<DecodeSmem*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], 1);
+    }
+    for (int i = 0; i < kScaleRing; ++i) mbar_init(&sm.sfull[i], 1);
+    for (int i = 0; i < kAcc; ++i) {
+      mbar_init(&sm.tfull[i], 1);
+      mbar_init(&sm.tempty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.qfull[i], 4);
+      mbar_init(&sm.qempty[i], 1 + 4);  // its products (a commit) and the epilogue's warps
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sm.rfull[i], 1);
+      mbar_init(&sm.rempty[i], 4 + 1 + 4);
+    }
+    sm.abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::);
+  }
+  if (warp == 1) tmem_alloc(&sm.tmem_base, kAcc * kHi);
+  if (HIST)
+    for (int i = tid; i < 2048; i += kDecThreads) sm.hist[i] = 0;
   pdl_wait();
-  const int r = row0 + blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const PagedGeom g = paged_geom(a.rows, r, blockIdx.x == 0 && threadIdx.x == 0);
-  const int64_t j0 = (int64_t)blockIdx.x * kKeysPerCta, j1 = min64(j0 + kKeysPerCta, g.nvis);
-  if (j0 >= j1) return;
-  for (int h = warp; h < kHi; h += kThreads / 32) {
-    const uint2 v = reinterpret_cast<const uint2*>(a.q_idx + ((int64_t)r * kHi + h) * kDi)[lane];
-    const uint32_t m = fold_max(absmax_bf16x2(absmax_bf16x2(0, v.x), v.y));
-    const bool fin = bf16_finite(m);
-    const int e = fin ? scale_exponent(m) : 0;
-    const float inv = fin ? pow2i(-e) : 0.f;
-    const float2 x = from_e4m3x2(fin ? e4m3x2(bf16_lo(v.x) * inv, bf16_hi(v.x) * inv) : 0);
-    const float2 y = from_e4m3x2(fin ? e4m3x2(bf16_lo(v.y) * inv, bf16_hi(v.y) * inv) : 0);
-    q[h][4 * lane] = x.x;
-    q[h][4 * lane + 1] = x.y;
-    q[h][4 * lane + 2] = y.x;
-    q[h][4 * lane + 3] = y.y;
-    if (lane == 0) wq[h] = fin ? a.w[(int64_t)r * kHi + h] * pow2i(e) : 0.f;
+
+  // This CTA's share of all rows' tiles.
+  const int n_rows = a.rows.n_rows, per = (n_rows + kDecThreads - 1) / kDecThreads;
+  const int r0 = min(tid * per, n_rows), r1 = min(r0 + per, n_rows);
+  unsigned long long mine = 0;
+  for (int r = r0; r < r1; ++r) mine += (unsigned long long)row_tiles(a.rows, r, blockIdx.x == 0);
+  sm.sums[tid] = mine;
+  __syncthreads();
+  if (warp == 0) {  // exclusive prefix over the 320 threads, ten a lane
+    unsigned long long s = 0;
+    for (int i = 0; i < 10; ++i) s += sm.sums[lane * 10 + i];
+    unsigned long long x = s;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const unsigned long long y = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += y;
+    }
+    if (lane == 31) sm.total = x;
+    x -= s;
+    for (int i = 0; i < 10; ++i) {
+      const unsigned long long v = sm.sums[lane * 10 + i];
+      sm.sums[lane * 10 + i] = x;
+      x += v;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const unsigned long long total = sm.total;
+  const unsigned long long first = total * blockIdx.x / gridDim.x, last = total * (blockIdx.x + 1) / gridDim.x;
+  const unsigned long long before = sm.sums[tid];
+  if (first < last && first >= before && first < before + mine) {
+    unsigned long long at = before;
+    for (int r = r0; r < r1; ++r) {
+      const unsigned long long n = (unsigned long long)row_tiles(a.rows, r, false);
+      if (first < at + n) {
+        sm.start_row = r;
+        sm.start_tile = (int)(first - at);
+        break;
+      }
+      at += n;
+    }
   }
   __syncthreads();
-  for (int64_t j = j0 + warp; j < j1; j += kThreads / 32) {
-    const int page = a.rows.block_table[(int64_t)g.seq * a.rows.max_pages + j / kPage];
-    const bool ok = page_ok(page, a.rows.n_pages);
-    float s = 0.f, sk = 0.f;
-    if (ok) {
-      const uint8_t* pg = a.key_pages + (int64_t)page * kKeyPage;
-      sk = reinterpret_cast<const float*>(pg + kPage * kDi)[j % kPage];
-      const uint32_t mine = reinterpret_cast<const uint32_t*>(pg + (j % kPage) * kDi)[lane];
-      float d = 0.f;
-      for (int c = 0; c < kDi / 4; ++c) {
-        const uint32_t k4 = __shfl_sync(0xffffffffu, mine, c);
-        const float2 x = from_e4m3x2(k4 & 0xffffu), y = from_e4m3x2(k4 >> 16);
-        d = fmaf(q[lane][4 * c], x.x, d);
-        d = fmaf(q[lane][4 * c + 1], x.y, d);
-        d = fmaf(q[lane][4 * c + 2], y.x, d);
-        d = fmaf(q[lane][4 * c + 3], y.y, d);
+  const uint32_t tmem = sm.tmem_base;
+  volatile int* abort_flag = &sm.abort_flag;
+  const bool work = first < last;
+
+  if (work && warp == 0) {
+    // ---------------- producer (and the rows' order, for the other roles) ----------------
+    unsigned long long left = last - first;
+    int t0 = sm.start_tile;
+    uint32_t g = 0, k = 0;
+    bool ok = true;
+    for (int r = sm.start_row; ok; ++r) {
+      RowInfo in = {-1, 0, 0, 0, 0};
+      if (left > 0 && r < n_rows) {
+        const PagedGeom geo = paged_geom(a.rows, r, false);
+        in.row = r;
+        in.seq = geo.seq;
+        in.nvis = geo.nvis;
+        in.t0 = t0;
+        in.t1 = (int)((geo.nvis + kTile - 1) / kTile);
+        if ((unsigned long long)(in.t1 - in.t0) > left) in.t1 = in.t0 + (int)left;
+        t0 = 0;
+        if (in.t0 >= in.t1) continue;  // a row without keys
       }
-      s = wq[lane] * fmaxf(d, 0.f);
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-      s = sk == sk ? s * sk : 0.f;
-    } else if (lane == 0) {
-      flag_error(a.rows.err, LSA_DEVERR_PAGE);
+      ok = k < 4 || mbar_wait_idle(&sm.rempty[k & 3], ((k >> 2) - 1) & 1, abort_flag);
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) {
+        sm.info[k & 3] = in;
+        mbar_arrive(&sm.rfull[k & 3]);
+      }
+      __syncwarp();
+      ++k;
+      if (in.row < 0) break;
+      left -= in.t1 - in.t0;
+      int pages = 0;
+      for (int t = in.t0; t < in.t1; ++t, ++g) {
+        const int in_batch = (t - in.t0) & 15;
+        if (in_batch == 0) pages = lookup_pages(a.rows, in.seq, in.nvis, 2 * (int64_t)t, lane);
+        const int p0 = __shfl_sync(0xffffffffu, pages, 2 * in_batch), p1 = __shfl_sync(0xffffffffu, pages, 2 * in_batch + 1);
+        const int s = g % kStages;
+        if (g >= kStages && !mbar_wait_idle(&sm.empty[s], ((g / kStages) - 1) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        __syncwarp();
+        if (lane == 0)
+          load_tile(&map, a.key_pages, p0, p1, sm.a[s], &sm.sc[g % kScaleRing], &sm.full[s], &sm.sfull[g % kScaleRing]);
+        __syncwarp();
+      }
     }
-    const bool forced = j < a.n_init || j >= g.nvis - a.n_loc;
-    if (lane == 0) a.scores[(int64_t)r * a.ld + j] = forced ? INFINITY : ok ? s : -INFINITY;
+    if (*abort_flag) drain_copies<kStages>(sm.full, sm.sfull, g);
+  } else if (work && warp == 1) {
+    // ---------------- MMA ----------------
+    const uint32_t leader = elect_one();
+    uint32_t g = 0;
+    bool ok = true;
+    for (uint32_t k = 0; ok; ++k) {
+      if (!mbar_wait_idle(&sm.rfull[k & 3], (k >> 2) & 1, abort_flag)) break;
+      const int n = sm.info[k & 3].row < 0 ? 0 : sm.info[k & 3].t1 - sm.info[k & 3].t0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.rempty[k & 3]);
+      if (n == 0 || !mbar_wait_idle(&sm.qfull[k & 1], (k >> 1) & 1, abort_flag)) break;
+      const uint64_t bd = sw128_desc(smem_u32(sm.q[k & 1]));
+      for (int i = 0; i < n; ++i, ++g) {
+        const int s = g % kStages, acc = g % kAcc;
+        if (!mbar_wait_idle(&sm.full[s], (g / kStages) & 1, abort_flag) ||
+            (g >= kAcc && !mbar_wait_idle(&sm.tempty[acc], ((g / kAcc) - 1) & 1, abort_flag))) {
+          ok = false;
+          break;
+        }
+        __syncwarp();
+        tc_fence_after();
+        const uint64_t ad = sw128_desc(smem_u32(sm.a[s]));
+#pragma unroll
+        for (int c = 0; c < kDi / 32; ++c)
+          umma_f8(tmem + acc * kHi, ad + (c * 32 >> 4), bd + (c * 32 >> 4), f8_idesc(kHi, false), c > 0 ? 1u : 0u, leader);
+        if (leader) {
+          umma_commit(&sm.tfull[acc]);
+          umma_commit(&sm.empty[s]);
+          if (i + 1 == n) umma_commit(&sm.qempty[k & 1]);
+        }
+        __syncwarp();
+      }
+    }
+  } else if (work && warp < 6) {
+    // ---------------- epilogue ----------------
+    const int quarter = warp & 3;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    uint32_t g = 0;
+    bool ok = true;  // after a wait that gave up the loops run on without storing
+    for (uint32_t k = 0;; ++k) {
+      ok = ok && mbar_wait_idle(&sm.rfull[k & 3], (k >> 2) & 1, abort_flag);
+      if (epilogue_any(!ok)) break;  // all four warps or none: they meet at the histogram
+      const RowInfo in = sm.info[k & 3];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.rempty[k & 3]);
+      if (in.row < 0) break;
+      ok = mbar_wait_idle(&sm.qfull[k & 1], (k >> 1) & 1, abort_flag);
+      float w[kHi];
+#pragma unroll
+      for (int h = 0; h < kHi; ++h) w[h] = sm.w[k & 1][h];
+      const bool hist_row = HIST && in.nvis > a.topk;
+      float* __restrict__ out = a.scores + (int64_t)in.row * a.ld;
+      for (int t = in.t0; t < in.t1; ++t, ++g) {
+        const int acc = g % kAcc, sr = g % kScaleRing;
+        ok = ok && mbar_wait_idle(&sm.sfull[sr], (g / kScaleRing) & 1, abort_flag);
+        const float sk = sm.sc[sr].s[quarter * 32 + lane];
+        const bool there = sm.sc[sr].ok[quarter >> 1] != 0;
+        ok = ok && mbar_wait_idle(&sm.tfull[acc], (g / kAcc) & 1, abort_flag);
+        __syncwarp();
+        tc_fence_after();
+        float v[kHi];
+        tmem_ld32(tmem + lanes + acc * kHi, v);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.tempty[acc]);
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int h = 0; h < kHi; h += 2) {
+          s0 = fmaf(w[h], fmaxf(v[h], 0.f), s0);
+          s1 = fmaf(w[h + 1], fmaxf(v[h + 1], 0.f), s1);
+        }
+        const int64_t j = (int64_t)t * kTile + quarter * 32 + lane;
+        if (ok && j < in.nvis) {
+          const bool forced = j < a.n_init || j >= in.nvis - a.n_loc;
+          const float x = there ? score_value(s0 + s1, sk) : -INFINITY;
+          out[j] = forced ? INFINITY : x;
+          if (HIST && hist_row && !forced) atomicAdd(&sm.hist[score_key(x) >> 21], 1u);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.qempty[k & 1]);
+      if (HIST) {  // the row's share of its histogram
+        asm volatile("bar.sync 1, 128;\n" ::: "memory");
+        if (hist_row) {
+          uint32_t* hr = a.hist + (int64_t)in.row * kTopkHistStride;
+          for (int i = (warp - 2) * 32 + lane; i < 2048; i += 128)
+            if (sm.hist[i]) {
+              atomicAdd(&hr[i], sm.hist[i]);
+              sm.hist[i] = 0;
+            }
+        }
+        asm volatile("bar.sync 1, 128;\n" ::: "memory");
+      }
+    }
+  } else if (work) {
+    // ---------------- queries (warps 6..9: heads 8 (warp - 6) ..) ----------------
+    const int h0 = (warp - 6) * 8 + (lane >> 4), sub = lane & 15;
+    for (uint32_t k = 0;; ++k) {
+      if (!mbar_wait_idle(&sm.rfull[k & 3], (k >> 2) & 1, abort_flag)) break;
+      const int r = sm.info[k & 3].row;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.rempty[k & 3]);
+      if (r < 0) break;
+      uint4 v[4];
+      float w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int h = h0 + 2 * i;
+        v[i] = __ldg(reinterpret_cast<const uint4*>(a.q_idx + ((int64_t)r * kHi + h) * kDi) + sub);
+        w[i] = __ldg(a.w + (int64_t)r * kHi + h);
+      }
+      if (k >= 2 && !mbar_wait_idle(&sm.qempty[k & 1], ((k >> 1) - 1) & 1, abort_flag)) break;
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int h = h0 + 2 * i;
+        float scale;
+        const uint2 c = quant_head(v[i], scale);
+        *reinterpret_cast<uint2*>(sm.q[k & 1] + h * kDi + (((sub >> 1) ^ (h & 7)) << 4) + (sub & 1) * 8) = c;
+        if (sub == 0) sm.w[k & 1][h] = scale == 0.f ? 0.f : w[i] * scale;
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.qfull[k & 1]);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && sm.abort_flag) flag_error(a.rows.err, LSA_DEVERR_TIMEOUT);
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kAcc * kHi);
   }
 }
 
-}  // namespace
+// ---------------------------------------------------------------- rows that share keys
 
-size_t fp8_index_ws_bytes(int n_rows, int n_seq) { return 0; }
+constexpr int kRows = 16;                     // rows of a CTA
+constexpr int kBStages = 6;
+constexpr int kEpiWarps = 8;
+constexpr int kBlkThreads = (2 + kEpiWarps) * 32;
+constexpr uint32_t kBHalf = 256 * kDi;        // 8 rows x 32 heads x 128 codes: 32 KB
 
-cudaError_t launch_fp8_index(const Fp8IndexArgs& a, cudaStream_t st) {
+struct __align__(1024) BlockSmem {
+  uint8_t b[2][kBHalf];
+  uint8_t a[kBStages][kTileBytes];
+  TileScales sc[kScaleRing];
+  __align__(16) float w[kRows][kHi];
+  int64_t nvis[kRows];
+  int seq[kRows];
+  // runs of rows of one sequence: its rows [run_r0, run_r1) of the block, its tiles
+  int run_r0[kRows], run_r1[kRows], run_tiles[kRows], n_runs;
+  uint64_t full[kBStages], empty[kBStages], sfull[kScaleRing], tfull[2], tempty[2], qfull;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+// The codes and weights of all rows' queries, a half warp a head.
+__global__ void __launch_bounds__(256) fp8_index_query_kernel(const __grid_constant__ Fp8IndexArgs a, uint8_t* codes, float* wq) {
+  pdl_wait();
+  const int64_t head = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 4;
+  const int sub = threadIdx.x & 15;
+  const bool live = head < (int64_t)a.rows.n_rows * kHi;
+  const uint4 v = live ? __ldg(reinterpret_cast<const uint4*>(a.q_idx + head * kDi) + sub) : make_uint4(0, 0, 0, 0);
+  float scale;
+  const uint2 c = quant_head(v, scale);
+  if (!live) return;
+  *reinterpret_cast<uint2*>(codes + head * kDi + sub * 8) = c;
+  if (sub == 0) wq[head] = scale == 0.f ? 0.f : a.w[head] * scale;
+}
+
+// Walks the CTA's tiles [t0, t1) of the block's runs, one after the other.
+struct RunCursor {
+  int run, tile;
+  __device__ __forceinline__ void start(const BlockSmem& sm, int t) {
+    run = 0;
+    tile = t;
+    while (run < sm.n_runs && tile >= sm.run_tiles[run]) tile -= sm.run_tiles[run++];
+  }
+  __device__ __forceinline__ void next(const BlockSmem& sm) {
+    ++tile;
+    while (run < sm.n_runs && tile >= sm.run_tiles[run]) {
+      tile = 0;
+      ++run;
+    }
+  }
+};
+
+// One CTA: 16 consecutive rows against a share of their key tiles. Warps: TMA
+// producer, MMA (tile x 8 rows x 32 heads twice, two 256-column accumulators),
+// eight epilogue warps (4 rows x 32 heads of an accumulator each; a thread = a
+// key). Rows of several sequences (a block that straddles prompts) take their
+// sequences' tiles one after the other.
+__global__ void __launch_bounds__(kBlkThreads, 1)
+    fp8_index_block_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap map_q,
+                           const __grid_constant__ Fp8IndexArgs a, const float* wq, int tiles_per_cta) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  if ((smem_u32(smem_raw) & 1023u) != 0) {
+    if (threadIdx.x == 0) flag_error(a.rows.err, LSA_DEVERR_TIMEOUT);
+    return;
+  }
+  BlockSmem& sm = *reinterpret_cast<BlockSmem*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();
+  // the latest blocks (of a causal chunk: the longest) first
+  const int row0 = (gridDim.x - 1 - blockIdx.x) * kRows;
+  if (tid < kRows) {
+    const int r = row0 + tid;
+    PagedGeom g = {-1, true, 0};
+    if (r < a.rows.n_rows) g = paged_geom(a.rows, r, blockIdx.y == 0);
+    sm.seq[tid] = g.seq;
+    sm.nvis[tid] = g.nvis;
+  }
+  for (int i = tid; i < kRows * kHi; i += kBlkThreads)
+    sm.w[i / kHi][i % kHi] = row0 + i / kHi < a.rows.n_rows ? wq[(int64_t)row0 * kHi + i] : 0.f;
+  if (tid == 0) {
+    for (int s = 0; s < kBStages; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    for (int i = 0; i < kScaleRing; ++i) mbar_init(&sm.sfull[i], 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sm.tfull[b], 1);
+      mbar_init(&sm.tempty[b], kEpiWarps);
+    }
+    mbar_init(&sm.qfull, 1);
+    sm.abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::);
+  }
+  __syncthreads();
+  if (tid == 0) {
+    int n = 0;
+    for (int i = 0; i < kRows;) {
+      int e = i + 1;
+      int64_t most = sm.nvis[i];
+      for (; e < kRows && sm.seq[e] == sm.seq[i]; ++e) most = max64(most, sm.nvis[e]);
+      if (sm.seq[i] >= 0 && most > 0) {
+        sm.run_r0[n] = i;
+        sm.run_r1[n] = e;
+        sm.run_tiles[n++] = (int)((most + kTile - 1) / kTile);
+      }
+      i = e;
+    }
+    sm.n_runs = n;
+  }
+  __syncthreads();
+  int64_t n_all = 0;
+  for (int i = 0; i < sm.n_runs; ++i) n_all += sm.run_tiles[i];
+  const int64_t t0 = (int64_t)blockIdx.y * tiles_per_cta;
+  const int n_tiles = (int)max64(0, min64(n_all - t0, blockIdx.y + 1 == gridDim.y ? n_all : (int64_t)tiles_per_cta));
+  if (n_tiles == 0) return;  // uniform across the CTA; nothing allocated yet
+  if (warp == 1) tmem_alloc(&sm.tmem_base, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  volatile int* abort_flag = &sm.abort_flag;
+
+  RunCursor cur;
+  cur.start(sm, (int)t0);
+  if (warp == 0) {
+    // ---------------- producer ----------------
+    if (lane == 0) {
+      mbar_expect_tx(&sm.qfull, 2 * kBHalf);
+      for (int q = 0; q < 2; ++q) tma_load_2d(sm.b[q], &map_q, 0, row0 * kHi + q * 256, &sm.qfull);
+    }
+    __syncwarp();
+    int pages = 0, batch_run = -1, batch = 0, i = 0;
+    int64_t most = 0;
+    for (; i < n_tiles; ++i, cur.next(sm)) {
+      if (cur.run != batch_run || cur.tile - batch >= 16) {
+        if (cur.run != batch_run) {
+          most = 0;
+          for (int r = sm.run_r0[cur.run]; r < sm.run_r1[cur.run]; ++r) most = max64(most, sm.nvis[r]);
+        }
+        batch_run = cur.run;
+        batch = cur.tile;
+        pages = lookup_pages(a.rows, sm.seq[sm.run_r0[cur.run]], most, 2 * (int64_t)batch, lane);
+      }
+      const int in_batch = cur.tile - batch;
+      const int p0 = __shfl_sync(0xffffffffu, pages, 2 * in_batch), p1 = __shfl_sync(0xffffffffu, pages, 2 * in_batch + 1);
+      const int s = i % kBStages;
+      if (i >= kBStages && !mbar_wait_idle(&sm.empty[s], ((i / kBStages) - 1) & 1, abort_flag)) break;
+      __syncwarp();
+      if (lane == 0)
+        load_tile(&map, a.key_pages, p0, p1, sm.a[s], &sm.sc[i % kScaleRing], &sm.full[s], &sm.sfull[i % kScaleRing]);
+      __syncwarp();
+    }
+    if (*abort_flag) {
+      drain_copies<kBStages>(sm.full, sm.sfull, i);
+      const long long t_out = global_ns();
+      while (!mbar_try_wait(&sm.qfull, 0) && global_ns() - t_out < kWaitLimitNs) {
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA ----------------
+    const uint32_t leader = elect_one();
+    bool ok = mbar_wait_idle(&sm.qfull, 0, abort_flag);
+    const uint32_t b_addr = smem_u32(sm.b[0]);
+    for (int i = 0; ok && i < n_tiles; ++i) {
+      const int s = i % kBStages;
+      if (!mbar_wait_idle(&sm.full[s], (i / kBStages) & 1, abort_flag)) break;
+      const uint64_t ad = sw128_desc(smem_u32(sm.a[s]));
+      for (int hb = 0; hb < 2; ++hb) {
+        if (i > 0 && !mbar_wait_idle(&sm.tempty[hb], (i - 1) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        __syncwarp();
+        tc_fence_after();
+        const uint64_t bd = sw128_desc(b_addr + hb * kBHalf);
+#pragma unroll
+        for (int c = 0; c < kDi / 32; ++c)
+          umma_f8(tmem + hb * 256, ad + (c * 32 >> 4), bd + (c * 32 >> 4), f8_idesc(256, false), c > 0 ? 1u : 0u, leader);
+        if (leader) {
+          umma_commit(&sm.tfull[hb]);
+          if (hb == 1) umma_commit(&sm.empty[s]);
+        }
+        __syncwarp();
+      }
+    }
+  } else {
+    // ---------------- epilogue (warps 2..9) ----------------
+    const int quarter = warp & 3, half = (warp - 2) >> 2;  // rows 4 half .. of an accumulator's 8
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    for (int i = 0; i < n_tiles; ++i, cur.next(sm)) {
+      const int sr = i % kScaleRing;
+      if (!mbar_wait_idle(&sm.sfull[sr], (i / kScaleRing) & 1, abort_flag)) break;
+      const float sk = sm.sc[sr].s[quarter * 32 + lane];
+      const bool there = sm.sc[sr].ok[quarter >> 1] != 0;
+      const int64_t j = (int64_t)cur.tile * kTile + quarter * 32 + lane;
+      const int r0 = sm.run_r0[cur.run], r1 = sm.run_r1[cur.run];
+      bool ok = true;
+      for (int hb = 0; hb < 2; ++hb) {
+        if (!mbar_wait_idle(&sm.tfull[hb], i & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        __syncwarp();
+        tc_fence_after();
+        float acc[4][32];
+        tmem_ld32_x4(tmem + lanes + hb * 256 + half * 128, 32, acc);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.tempty[hb]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int row = hb * 8 + half * 4 + u;
+          if (row < r0 || row >= r1) continue;
+          float s0 = 0.f, s1 = 0.f;
+          const float4* wv = reinterpret_cast<const float4*>(sm.w[row]);
+#pragma unroll
+          for (int h4 = 0; h4 < 8; ++h4) {
+            const float4 w = wv[h4];
+            s0 = fmaf(w.x, fmaxf(acc[u][4 * h4 + 0], 0.f), s0);
+            s1 = fmaf(w.y, fmaxf(acc[u][4 * h4 + 1], 0.f), s1);
+            s0 = fmaf(w.z, fmaxf(acc[u][4 * h4 + 2], 0.f), s0);
+            s1 = fmaf(w.w, fmaxf(acc[u][4 * h4 + 3], 0.f), s1);
+          }
+          const int64_t nvis = sm.nvis[row];
+          if (j < nvis) {
+            const bool forced = j < a.n_init || j >= nvis - a.n_loc;
+            a.scores[(int64_t)(row0 + row) * a.ld + j] = forced ? INFINITY : there ? score_value(s0 + s1, sk) : -INFINITY;
+          }
+        }
+      }
+      if (!ok) break;
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && sm.abort_flag) flag_error(a.rows.err, LSA_DEVERR_TIMEOUT);
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+bool use_blocks(int n_rows, int n_seq) { return n_rows >= 8 && (int64_t)n_rows >= 4 * (int64_t)n_seq; }
+
+int sm_count() {
+  static int cache[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+  if (cache[dev] == 0) {
+    int s = 148;
+    if (cudaDeviceGetAttribute(&s, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || s < 1) s = 148;
+    cache[dev] = s;
+  }
+  return cache[dev];
+}
+
+template <typename K>
+cudaError_t set_smem(K kernel, int bytes, bool (&done)[64]) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || done[dev]) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done[dev] = true;
+  return e;
+}
+
+// Key pages: 64 rows of 128 codes, pages kKeyPage bytes apart; a box is one page.
+bool page_map(CUtensorMap* m, const void* base, int n_pages) {
+  const auto fn = tensor_map_encode();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {kDi, kPage, (cuuint64_t)n_pages};
+  const cuuint64_t strides[2] = {kDi, kKeyPage};
+  const cuuint32_t box[3] = {kDi, kPage, 1}, step[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Query codes: n rows of 128, a box is 256 of them.
+bool query_map(CUtensorMap* m, const void* base, int64_t n) {
+  const auto fn = tensor_map_encode();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {kDi, (cuuint64_t)n};
+  const cuuint64_t strides[1] = {kDi};
+  const cuuint32_t box[2] = {kDi, 256}, step[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t launch_rows(const Fp8IndexArgs& a, const CUtensorMap& map, cudaStream_t st) {
+  static bool done[2][64];
+  const int64_t most = (int64_t)a.rows.n_rows * ((a.rows.max_len + kTile - 1) / kTile);
+  const dim3 grid((unsigned)max64(1, min64(most, sm_count())));
+  const int smem = (int)sizeof(DecodeSmem);
+  cudaError_t e;
   if (a.hist) {
-    const cudaError_t e = launch_zero_words(a.hist, (size_t)a.rows.n_rows * kTopkHistStride, st);
-    if (e != cudaSuccess) return e;
+    e = launch_zero_words(a.hist, (size_t)a.rows.n_rows * kTopkHistStride, st);
+    if (e == cudaSuccess) e = set_smem(fp8_index_rows_kernel<true>, smem, done[0]);
+    if (e == cudaSuccess) e = launch_pdl(fp8_index_rows_kernel<true>, grid, dim3(kDecThreads), smem, st, map, a);
+  } else {
+    e = set_smem(fp8_index_rows_kernel<false>, smem, done[1]);
+    if (e == cudaSuccess) e = launch_pdl(fp8_index_rows_kernel<false>, grid, dim3(kDecThreads), smem, st, map, a);
   }
-  const unsigned nx = (unsigned)((a.rows.max_len + kKeysPerCta - 1) / kKeysPerCta);
-  for (int row0 = 0; row0 < a.rows.n_rows; row0 += 65535) {
-    const cudaError_t e = launch_pdl(fp8_index_simple_kernel, dim3(nx, (unsigned)min(65535, a.rows.n_rows - row0)),
-                                     dim3(kThreads), 0, st, a, row0);
-    if (e != cudaSuccess) return e;
-    count_launches(1);
-  }
+  count_launches(1);
+  return e;
+}
+
+cudaError_t launch_blocks(const Fp8IndexArgs& a, const CUtensorMap& map, cudaStream_t st) {
+  static bool done[64];
+  const int n_rows = a.rows.n_rows;
+  uint8_t* codes = static_cast<uint8_t*>(a.ws);
+  float* wq = reinterpret_cast<float*>(codes + (size_t)n_rows * kHi * kDi);
+  CUtensorMap map_q;
+  if (!query_map(&map_q, codes, (int64_t)n_rows * kHi)) return cudaErrorInvalidValue;
+  cudaError_t e = launch_pdl(fp8_index_query_kernel, dim3((unsigned)(((int64_t)n_rows * kHi * 16 + 255) / 256)), dim3(256), 0,
+                             st, a, codes, wq);
+  count_launches(1);
+  if (e != cudaSuccess) return e;
+  e = set_smem(fp8_index_block_kernel, (int)sizeof(BlockSmem), done);
+  if (e != cudaSuccess) return e;
+  // Shares of the tiles: enough CTAs to fill the SMs a few times over, at least 16
+  // tiles each (a CTA's start, with its 64 KB of queries, costs about three).
+  const int n_blocks = (n_rows + kRows - 1) / kRows;
+  const int64_t tiles = (a.rows.max_len + kTile - 1) / kTile;
+  const int64_t want = max64(1, (4LL * sm_count() + n_blocks - 1) / n_blocks);
+  const int64_t per = max64(16, (tiles + want - 1) / want), chunks = (tiles + per - 1) / per;
+  e = launch_pdl(fp8_index_block_kernel, dim3((unsigned)n_blocks, (unsigned)chunks), dim3(kBlkThreads), sizeof(BlockSmem),
+                 st, map, map_q, a, (const float*)wq, (int)per);
+  count_launches(1);
+  if (e != cudaSuccess) return e;
   if (!a.hist) return cudaSuccess;
+  // The epilogue has no room for histograms: one pass over the fresh scores builds them.
+  e = launch_zero_words(a.hist, (size_t)n_rows * kTopkHistStride, st);
+  if (e != cudaSuccess) return e;
   TopkArgs t;
   t.scores = a.scores;
   t.ld = a.ld;
   t.pos = a.rows.pos;
-  t.n_rows = a.rows.n_rows;
+  t.n_rows = n_rows;
   t.max_len = a.rows.max_len;
   t.topk = a.topk;
   t.n_init = a.n_init;
@@ -104,6 +760,18 @@ cudaError_t launch_fp8_index(const Fp8IndexArgs& a, cudaStream_t st) {
   t.ws = nullptr;
   t.ws_bytes = 0;
   return launch_topk_hist_only(t, a.hist, st);
+}
+
+}  // namespace
+
+size_t fp8_index_ws_bytes(int n_rows, int n_seq) {
+  return use_blocks(n_rows, n_seq) ? (size_t)n_rows * kHi * (kDi + sizeof(float)) : 0;
+}
+
+cudaError_t launch_fp8_index(const Fp8IndexArgs& a, cudaStream_t st) {
+  CUtensorMap map;
+  if (!page_map(&map, a.key_pages, a.rows.n_pages)) return cudaErrorInvalidValue;
+  return use_blocks(a.rows.n_rows, a.rows.n_seq) ? launch_blocks(a, map, st) : launch_rows(a, map, st);
 }
 
 }  // namespace lsa

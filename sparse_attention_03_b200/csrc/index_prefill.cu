@@ -237,7 +237,9 @@ done:
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+}  // namespace
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encode() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   if (!fn) {
     void* p = nullptr;
@@ -249,9 +251,11 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+namespace {
+
 // 2D bf16 map over [rows, 128] with a box of box_rows x 64 and 128-byte swizzle.
 bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows) {
-  auto fn = encode_fn();
+  auto fn = tensor_map_encode();
   if (!fn) return false;
   cuuint64_t dims[2] = {(cuuint64_t)kDi, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)kDi * 2};
@@ -266,7 +270,7 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows
 
 bool index_prefill_supported(const IndexArgs& a) {
   return a.k_off == nullptr && a.n_seq == 1 && a.seq_of_row == nullptr && a.pos_div == 1 && a.n_rows >= kRowsPerBlock &&
-         encode_fn() != nullptr;
+         tensor_map_encode() != nullptr;
 }
 
 cudaError_t launch_index_prefill(const IndexArgs& a, cudaStream_t st) {
