@@ -73,6 +73,35 @@ __device__ __forceinline__ int lookup_pages(const PagedRows& rows, int seq, int6
 
 __device__ __forceinline__ float score_value(float s, float sk) { return sk == sk ? s * sk : 0.f; }
 
+// s += w * (x0, x1), two fp32 in one register pair; and the sum of two such pairs.
+__device__ __forceinline__ void fma_pair(unsigned long long& s, unsigned long long w, float x0, float x1) {
+  asm("{\n .reg .b64 x;\n mov.b64 x, {%2, %3};\n fma.rn.f32x2 %0, %1, x, %0;\n}\n" : "+l"(s) : "l"(w), "f"(x0), "f"(x1));
+}
+__device__ __forceinline__ float sum_pairs(unsigned long long a, unsigned long long b) {
+  float a0, a1, b0, b1;
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a0), "=f"(a1) : "l"(a));
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(b0), "=f"(b1) : "l"(b));
+  return (a0 + a1) + (b0 + b1);
+}
+
+// One row's ReLU-weighted sum over its 32 heads, w holding half the weights: the
+// ReLU as x + |x| = 2 max(x, 0), one addition at full rate (32 maxima and their
+// FMAs took 188 cycles a warp with four warps a scheduler, the additions 141),
+// then two heads an instruction (packed fp32 pairs, four chains).
+__device__ __forceinline__ float weighted_sum(const uint32_t (&v)[32], const float* w) {
+  unsigned long long s[4] = {0, 0, 0, 0};
+  const ulonglong2* wv = reinterpret_cast<const ulonglong2*>(w);
+#pragma unroll
+  for (int h4 = 0; h4 < 8; ++h4) {
+    const ulonglong2 ww = wv[h4];
+    const float x0 = __uint_as_float(v[4 * h4]), x1 = __uint_as_float(v[4 * h4 + 1]);
+    const float x2 = __uint_as_float(v[4 * h4 + 2]), x3 = __uint_as_float(v[4 * h4 + 3]);
+    fma_pair(s[2 * (h4 & 1)], ww.x, x0 + fabsf(x0), x1 + fabsf(x1));
+    fma_pair(s[2 * (h4 & 1) + 1], ww.y, x2 + fabsf(x2), x3 + fabsf(x3));
+  }
+  return sum_pairs(s[0], s[1]) + sum_pairs(s[2], s[3]);
+}
+
 // Quantises one head's 128 query elements over a half warp (8 elements a lane,
 // sub = lane & 15): the codes and the scale (NaN vectors: zeros and 0).
 __device__ __forceinline__ uint2 quant_head(uint4 v, float& scale) {
@@ -88,7 +117,7 @@ __device__ __forceinline__ uint2 quant_head(uint4 v, float& scale) {
 
 // ---------------------------------------------------------------- rows of their own
 
-constexpr int kStages = 8;      // 128 KB of keys in flight
+constexpr int kStages = 5;      // 80 KB of keys in flight a CTA, two CTAs an SM
 constexpr int kAcc = 4;         // accumulators of 32 columns
 constexpr int kDecThreads = 10 * 32;
 
@@ -145,7 +174,7 @@ __device__ __forceinline__ void drain_copies(uint64_t* full, uint64_t* sfull, ui
 // (tiles of consecutive rows). Warps: producer, MMA, four for the epilogue (a
 // thread = a key), four for the rows' queries.
 template <bool HIST>
-__global__ void __launch_bounds__(kDecThreads, 1)
+__global__ void __launch_bounds__(kDecThreads, 2)
     fp8_index_rows_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ Fp8IndexArgs a) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   if ((smem_u32(smem_raw) & 1023u) != 0) {
@@ -246,7 +275,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         t0 = 0;
         if (in.t0 >= in.t1) continue;  // a row without keys
       }
-      ok = k < 4 || mbar_wait_idle(&sm.rempty[k & 3], ((k >> 2) - 1) & 1, abort_flag);
+      ok = k < 4 || mbar_wait_fast(&sm.rempty[k & 3], ((k >> 2) - 1) & 1, abort_flag);
       if (!ok) break;
       __syncwarp();
       if (lane == 0) {
@@ -263,7 +292,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         if (in_batch == 0) pages = lookup_pages(a.rows, in.seq, in.nvis, 2 * (int64_t)t, lane);
         const int p0 = __shfl_sync(0xffffffffu, pages, 2 * in_batch), p1 = __shfl_sync(0xffffffffu, pages, 2 * in_batch + 1);
         const int s = g % kStages;
-        if (g >= kStages && !mbar_wait_idle(&sm.empty[s], ((g / kStages) - 1) & 1, abort_flag)) {
+        if (g >= kStages && !mbar_wait_fast(&sm.empty[s], ((g / kStages) - 1) & 1, abort_flag)) {
           ok = false;
           break;
         }
@@ -280,16 +309,16 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     uint32_t g = 0;
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
-      if (!mbar_wait_idle(&sm.rfull[k & 3], (k >> 2) & 1, abort_flag)) break;
+      if (!mbar_wait_fast(&sm.rfull[k & 3], (k >> 2) & 1, abort_flag)) break;
       const int n = sm.info[k & 3].row < 0 ? 0 : sm.info[k & 3].t1 - sm.info[k & 3].t0;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.rempty[k & 3]);
-      if (n == 0 || !mbar_wait_idle(&sm.qfull[k & 1], (k >> 1) & 1, abort_flag)) break;
+      if (n == 0 || !mbar_wait_fast(&sm.qfull[k & 1], (k >> 1) & 1, abort_flag)) break;
       const uint64_t bd = sw128_desc(smem_u32(sm.q[k & 1]));
       for (int i = 0; i < n; ++i, ++g) {
         const int s = g % kStages, acc = g % kAcc;
-        if (!mbar_wait_idle(&sm.full[s], (g / kStages) & 1, abort_flag) ||
-            (g >= kAcc && !mbar_wait_idle(&sm.tempty[acc], ((g / kAcc) - 1) & 1, abort_flag))) {
+        if (!mbar_wait_fast(&sm.full[s], (g / kStages) & 1, abort_flag) ||
+            (g >= kAcc && !mbar_wait_fast(&sm.tempty[acc], ((g / kAcc) - 1) & 1, abort_flag))) {
           ok = false;
           break;
         }
@@ -314,13 +343,13 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     uint32_t g = 0;
     bool ok = true;  // after a wait that gave up the loops run on without storing
     for (uint32_t k = 0;; ++k) {
-      ok = ok && mbar_wait_idle(&sm.rfull[k & 3], (k >> 2) & 1, abort_flag);
+      ok = ok && mbar_wait_fast(&sm.rfull[k & 3], (k >> 2) & 1, abort_flag);
       if (epilogue_any(!ok)) break;  // all four warps or none: they meet at the histogram
       const RowInfo in = sm.info[k & 3];
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.rempty[k & 3]);
       if (in.row < 0) break;
-      ok = mbar_wait_idle(&sm.qfull[k & 1], (k >> 1) & 1, abort_flag);
+      ok = mbar_wait_fast(&sm.qfull[k & 1], (k >> 1) & 1, abort_flag);
       float w[kHi];
 #pragma unroll
       for (int h = 0; h < kHi; ++h) w[h] = sm.w[k & 1][h];
@@ -328,10 +357,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       float* __restrict__ out = a.scores + (int64_t)in.row * a.ld;
       for (int t = in.t0; t < in.t1; ++t, ++g) {
         const int acc = g % kAcc, sr = g % kScaleRing;
-        ok = ok && mbar_wait_idle(&sm.sfull[sr], (g / kScaleRing) & 1, abort_flag);
+        ok = ok && mbar_wait_fast(&sm.sfull[sr], (g / kScaleRing) & 1, abort_flag);
         const float sk = sm.sc[sr].s[quarter * 32 + lane];
         const bool there = sm.sc[sr].ok[quarter >> 1] != 0;
-        ok = ok && mbar_wait_idle(&sm.tfull[acc], (g / kAcc) & 1, abort_flag);
+        ok = ok && mbar_wait_fast(&sm.tfull[acc], (g / kAcc) & 1, abort_flag);
         __syncwarp();
         tc_fence_after();
         float v[kHi];
@@ -372,7 +401,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     // ---------------- queries (warps 6..9: heads 8 (warp - 6) ..) ----------------
     const int h0 = (warp - 6) * 8 + (lane >> 4), sub = lane & 15;
     for (uint32_t k = 0;; ++k) {
-      if (!mbar_wait_idle(&sm.rfull[k & 3], (k >> 2) & 1, abort_flag)) break;
+      if (!mbar_wait_fast(&sm.rfull[k & 3], (k >> 2) & 1, abort_flag)) break;
       const int r = sm.info[k & 3].row;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.rempty[k & 3]);
@@ -385,7 +414,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         v[i] = __ldg(reinterpret_cast<const uint4*>(a.q_idx + ((int64_t)r * kHi + h) * kDi) + sub);
         w[i] = __ldg(a.w + (int64_t)r * kHi + h);
       }
-      if (k >= 2 && !mbar_wait_idle(&sm.qempty[k & 1], ((k >> 1) - 1) & 1, abort_flag)) break;
+      if (k >= 2 && !mbar_wait_fast(&sm.qempty[k & 1], ((k >> 1) - 1) & 1, abort_flag)) break;
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -414,8 +443,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 
 constexpr int kRows = 16;                     // rows of a CTA
 constexpr int kBStages = 6;
-constexpr int kEpiWarps = 8;
-constexpr int kBlkThreads = (2 + kEpiWarps) * 32;
+constexpr int kEpiWarps = 16;
+static_assert(8 * 4 / kEpiWarps == 2, "rows of an accumulator that a warp sums");
+constexpr int kProducer = kEpiWarps, kMma = kEpiWarps + 1;  // their warps
+constexpr int kBlkThreads = (kEpiWarps + 2) * 32;
 constexpr uint32_t kBHalf = 256 * kDi;        // 8 rows x 32 heads x 128 codes: 32 KB
 
 struct __align__(1024) BlockSmem {
@@ -463,10 +494,9 @@ struct RunCursor {
   }
 };
 
-// One CTA: 16 consecutive rows against a share of their key tiles. Warps: TMA
-// producer, MMA (tile x 8 rows x 32 heads twice, two 256-column accumulators),
-// eight epilogue warps (4 rows x 32 heads of an accumulator each; a thread = a
-// key). Rows of several sequences (a block that straddles prompts) take their
+// One CTA: 16 consecutive rows against a share of their key tiles. Warps: sixteen
+// for the epilogue (2 rows x 32 heads of an accumulator each; a thread = a key), TMA
+// producer, MMA (tile x 8 rows x 32 heads twice, two 256-column accumulators). Rows of several sequences (a block that straddles prompts) take their
 // sequences' tiles one after the other.
 __global__ void __launch_bounds__(kBlkThreads, 1)
     fp8_index_block_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap map_q,
@@ -489,7 +519,7 @@ __global__ void __launch_bounds__(kBlkThreads, 1)
     sm.nvis[tid] = g.nvis;
   }
   for (int i = tid; i < kRows * kHi; i += kBlkThreads)
-    sm.w[i / kHi][i % kHi] = row0 + i / kHi < a.rows.n_rows ? wq[(int64_t)row0 * kHi + i] : 0.f;
+    sm.w[i / kHi][i % kHi] = row0 + i / kHi < a.rows.n_rows ? 0.5f * wq[(int64_t)row0 * kHi + i] : 0.f;
   if (tid == 0) {
     for (int s = 0; s < kBStages; ++s) {
       mbar_init(&sm.full[s], 1);
@@ -526,7 +556,7 @@ __global__ void __launch_bounds__(kBlkThreads, 1)
   const int64_t t0 = (int64_t)blockIdx.y * tiles_per_cta;
   const int n_tiles = (int)max64(0, min64(n_all - t0, blockIdx.y + 1 == gridDim.y ? n_all : (int64_t)tiles_per_cta));
   if (n_tiles == 0) return;  // uniform across the CTA; nothing allocated yet
-  if (warp == 1) tmem_alloc(&sm.tmem_base, 512);
+  if (warp == kMma) tmem_alloc(&sm.tmem_base, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -535,7 +565,7 @@ __global__ void __launch_bounds__(kBlkThreads, 1)
 
   RunCursor cur;
   cur.start(sm, (int)t0);
-  if (warp == 0) {
+  if (warp == kProducer) {
     // ---------------- producer ----------------
     if (lane == 0) {
       mbar_expect_tx(&sm.qfull, 2 * kBHalf);
@@ -557,7 +587,7 @@ __global__ void __launch_bounds__(kBlkThreads, 1)
       const int in_batch = cur.tile - batch;
       const int p0 = __shfl_sync(0xffffffffu, pages, 2 * in_batch), p1 = __shfl_sync(0xffffffffu, pages, 2 * in_batch + 1);
       const int s = i % kBStages;
-      if (i >= kBStages && !mbar_wait_idle(&sm.empty[s], ((i / kBStages) - 1) & 1, abort_flag)) break;
+      if (i >= kBStages && !mbar_wait_fast(&sm.empty[s], ((i / kBStages) - 1) & 1, abort_flag)) break;
       __syncwarp();
       if (lane == 0)
         load_tile(&map, a.key_pages, p0, p1, sm.a[s], &sm.sc[i % kScaleRing], &sm.full[s], &sm.sfull[i % kScaleRing]);
@@ -569,17 +599,17 @@ __global__ void __launch_bounds__(kBlkThreads, 1)
       while (!mbar_try_wait(&sm.qfull, 0) && global_ns() - t_out < kWaitLimitNs) {
       }
     }
-  } else if (warp == 1) {
+  } else if (warp == kMma) {
     // ---------------- MMA ----------------
     const uint32_t leader = elect_one();
-    bool ok = mbar_wait_idle(&sm.qfull, 0, abort_flag);
+    bool ok = mbar_wait_fast(&sm.qfull, 0, abort_flag);
     const uint32_t b_addr = smem_u32(sm.b[0]);
     for (int i = 0; ok && i < n_tiles; ++i) {
       const int s = i % kBStages;
-      if (!mbar_wait_idle(&sm.full[s], (i / kBStages) & 1, abort_flag)) break;
+      if (!mbar_wait_fast(&sm.full[s], (i / kBStages) & 1, abort_flag)) break;
       const uint64_t ad = sw128_desc(smem_u32(sm.a[s]));
       for (int hb = 0; hb < 2; ++hb) {
-        if (i > 0 && !mbar_wait_idle(&sm.tempty[hb], (i - 1) & 1, abort_flag)) {
+        if (i > 0 && !mbar_wait_fast(&sm.tempty[hb], (i - 1) & 1, abort_flag)) {
           ok = false;
           break;
         }
@@ -596,59 +626,91 @@ __global__ void __launch_bounds__(kBlkThreads, 1)
         __syncwarp();
       }
     }
-  } else {
-    // ---------------- epilogue (warps 2..9) ----------------
-    const int quarter = warp & 3, half = (warp - 2) >> 2;  // rows 4 half .. of an accumulator's 8
+  } else if (warp < kEpiWarps) {
+    // ---------------- epilogue ----------------
+    const int quarter = warp & 3, part = warp >> 2;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    for (int i = 0; i < n_tiles; ++i, cur.next(sm)) {
+    const int lane_j = quarter * 32 + lane;
+    // This warp's rows: 2 part and 2 part + 1 of each accumulator.
+    float* out[4];
+    int32_t nvis[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int row = (u >> 1) * 8 + part * 2 + (u & 1);
+      out[u] = a.scores + (int64_t)(row0 + row) * a.ld + lane_j;
+      nvis[u] = (int32_t)min64(sm.nvis[row], INT32_MAX);
+    }
+    int run = -1, tiles_left = 0, mine = 0, lo_key = 0, hi_key = 0;
+    for (int i = 0; i < n_tiles; ++i) {
+      if (tiles_left == 0) {  // a run begins: which of the warp's rows are in it, and the keys that no row treats apart
+        run = cur.run;
+        const int r0 = sm.run_r0[run], r1 = sm.run_r1[run];
+        tiles_left = sm.run_tiles[run] - cur.tile;
+        mine = 0;
+        lo_key = a.n_init;
+        hi_key = INT32_MAX;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int row = (u >> 1) * 8 + part * 2 + (u & 1);
+          if (row >= r0 && row < r1) {
+            mine |= 1 << u;
+            hi_key = min(hi_key, max(nvis[u] - a.n_loc, 0));
+          }
+        }
+      }
       const int sr = i % kScaleRing;
-      if (!mbar_wait_idle(&sm.sfull[sr], (i / kScaleRing) & 1, abort_flag)) break;
-      const float sk = sm.sc[sr].s[quarter * 32 + lane];
+      if (!mbar_wait_fast(&sm.sfull[sr], (i / kScaleRing) & 1, abort_flag)) break;
       const bool there = sm.sc[sr].ok[quarter >> 1] != 0;
-      const int64_t j = (int64_t)cur.tile * kTile + quarter * 32 + lane;
-      const int r0 = sm.run_r0[cur.run], r1 = sm.run_r1[cur.run];
+      const float sk = score_value(1.f, sm.sc[sr].s[lane_j]);
+      const int first = cur.tile * kTile;
+      // Most tiles: every key is there, visible to every row of the warp and forced for none.
+      const bool plain = there && mine == 15 && first >= lo_key && first <= hi_key - kTile;
       bool ok = true;
+#pragma unroll
       for (int hb = 0; hb < 2; ++hb) {
-        if (!mbar_wait_idle(&sm.tfull[hb], i & 1, abort_flag)) {
+        if (!mbar_wait_fast(&sm.tfull[hb], i & 1, abort_flag)) {
           ok = false;
           break;
         }
         __syncwarp();
         tc_fence_after();
-        float acc[4][32];
-        tmem_ld32_x4(tmem + lanes + hb * 256 + half * 128, 32, acc);
+        // Two rows of this accumulator; it goes back to the MMA warp before the sums.
+        const uint32_t at = tmem + lanes + hb * 256 + part * 64;
+        uint32_t v[2][32];
+        tmem_ld32_request(at, v[0]);
+        tmem_ld32_request(at + 32, v[1]);
+        tmem_ld32_wait(v[0]);
+        tmem_ld32_wait(v[1]);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.tempty[hb]);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int row = hb * 8 + half * 4 + u;
-          if (row < r0 || row >= r1) continue;
-          float s0 = 0.f, s1 = 0.f;
-          const float4* wv = reinterpret_cast<const float4*>(sm.w[row]);
-#pragma unroll
-          for (int h4 = 0; h4 < 8; ++h4) {
-            const float4 w = wv[h4];
-            s0 = fmaf(w.x, fmaxf(acc[u][4 * h4 + 0], 0.f), s0);
-            s1 = fmaf(w.y, fmaxf(acc[u][4 * h4 + 1], 0.f), s1);
-            s0 = fmaf(w.z, fmaxf(acc[u][4 * h4 + 2], 0.f), s0);
-            s1 = fmaf(w.w, fmaxf(acc[u][4 * h4 + 3], 0.f), s1);
-          }
-          const int64_t nvis = sm.nvis[row];
-          if (j < nvis) {
-            const bool forced = j < a.n_init || j >= nvis - a.n_loc;
-            a.scores[(int64_t)(row0 + row) * a.ld + j] = forced ? INFINITY : there ? score_value(s0 + s1, sk) : -INFINITY;
+        for (int k = 0; k < 2; ++k) {
+          const int u = 2 * hb + k;
+          if (!(mine >> u & 1)) continue;
+          const float x = weighted_sum(v[k], sm.w[hb * 8 + part * 2 + k]) * sk;
+          if (plain) {
+            out[u][first] = x;
+          } else {
+            const int j = first + lane_j;
+            if (j < nvis[u])
+              out[u][first] = j < a.n_init || j >= nvis[u] - a.n_loc ? INFINITY : there ? x : -INFINITY;
           }
         }
       }
       if (!ok) break;
+      ++cur.tile;
+      if (--tiles_left == 0) {
+        --cur.tile;
+        cur.next(sm);
+      }
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && sm.abort_flag) flag_error(a.rows.err, LSA_DEVERR_TIMEOUT);
-  if (warp == 1) {
+  if (warp == kMma) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -704,7 +766,7 @@ bool query_map(CUtensorMap* m, const void* base, int64_t n) {
 cudaError_t launch_rows(const Fp8IndexArgs& a, const CUtensorMap& map, cudaStream_t st) {
   static bool done[2][64];
   const int64_t most = (int64_t)a.rows.n_rows * ((a.rows.max_len + kTile - 1) / kTile);
-  const dim3 grid((unsigned)max64(1, min64(most, sm_count())));
+  const dim3 grid((unsigned)max64(1, min64(most, 2LL * sm_count())));
   const int smem = (int)sizeof(DecodeSmem);
   cudaError_t e;
   if (a.hist) {
@@ -732,12 +794,22 @@ cudaError_t launch_blocks(const Fp8IndexArgs& a, const CUtensorMap& map, cudaStr
   if (e != cudaSuccess) return e;
   e = set_smem(fp8_index_block_kernel, (int)sizeof(BlockSmem), done);
   if (e != cudaSuccess) return e;
-  // Shares of the tiles: enough CTAs to fill the SMs a few times over, at least 16
-  // tiles each (a CTA's start, with its 64 KB of queries, costs about three).
+  // Shares of the tiles: the count whose waves of CTAs end first, a CTA's start
+  // (with its 64 KB of queries) costing about three tiles; at least 16 tiles each.
   const int n_blocks = (n_rows + kRows - 1) / kRows;
   const int64_t tiles = (a.rows.max_len + kTile - 1) / kTile;
-  const int64_t want = max64(1, (4LL * sm_count() + n_blocks - 1) / n_blocks);
-  const int64_t per = max64(16, (tiles + want - 1) / want), chunks = (tiles + per - 1) / per;
+  const int sms = sm_count();
+  const int64_t lo = max64(1, min64((2LL * sms + n_blocks - 1) / n_blocks, tiles / 16));
+  int64_t per = tiles, chunks = 1, best = INT64_MAX;
+  for (int64_t c = lo; c <= 4 * lo && c <= max64(1, tiles / 16); ++c) {
+    const int64_t p = (tiles + c - 1) / c, n = (tiles + p - 1) / p;
+    const int64_t cost = ((n * n_blocks + sms - 1) / sms) * (p + 3);  // waves of CTAs, each its tiles and its start
+    if (cost < best) {
+      best = cost;
+      per = p;
+      chunks = n;
+    }
+  }
   e = launch_pdl(fp8_index_block_kernel, dim3((unsigned)n_blocks, (unsigned)chunks), dim3(kBlkThreads), sizeof(BlockSmem),
                  st, map, map_q, a, (const float*)wq, (int)per);
   count_launches(1);

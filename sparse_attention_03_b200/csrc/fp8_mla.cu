@@ -241,8 +241,8 @@ struct Done {
 __device__ __forceinline__ bool write_out(const Fp8MlaArgs& a, const Split& sp, Fp8MlaSmem& sm, uint32_t tmem,
                                           const Done& done, int warp, int lane, float* part_o, float2* part_ml,
                                           volatile int* abort_flag) {
-  if (!mbar_wait(&sm.fin_full[done.nk & 3], (done.nk >> 2) & 1, abort_flag)) return false;
-  if (!mbar_wait(&sm.o_full, done.nk & 1, abort_flag)) return false;
+  if (!mbar_wait_fast(&sm.fin_full[done.nk & 3], (done.nk >> 2) & 1, abort_flag)) return false;
+  if (!mbar_wait_fast(&sm.o_full, done.nk & 1, abort_flag)) return false;
   __syncwarp();
   tc_fence_after();
   const int z = item_sub(a, sp, done.item), r = item_row(a, sp, done.item);
@@ -384,7 +384,7 @@ __device__ __forceinline__ void gather_role(const Fp8MlaArgs& a, const Split& sp
 #pragma unroll
     for (int cc = 0; cc < kChunks; ++cc) {
       const int c = cc == 0 ? 4 : cc - 1;
-      if (g >= 2 && !mbar_wait(c == 4 ? &sm.s_empty[b] : &sm.pv_done[b][c & 3], ((g >> 1) - 1) & 1, abort_flag)) return;
+      if (g >= 2 && !mbar_wait_fast(c == 4 ? &sm.s_empty[b] : &sm.pv_done[b][c & 3], ((g >> 1) - 1) & 1, abort_flag)) return;
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < kGroups; ++j) {
@@ -396,7 +396,7 @@ __device__ __forceinline__ void gather_role(const Fp8MlaArgs& a, const Split& sp
       cp_async_arrive(&sm.full[b][c]);
     }
     if (cur.first) {
-      if (nk > 0 && !mbar_wait(&sm.q_empty, (nk - 1) & 1, abort_flag)) return;
+      if (nk > 0 && !mbar_wait_fast(&sm.q_empty, (nk - 1) & 1, abort_flag)) return;
       __syncwarp();
       prepare_q(a, sp, sm, cur.item, nk, warp, lane);
     }
@@ -583,13 +583,13 @@ __device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& s
       const int b = g & 1;
       bool ok = true;
       if (t == t0) {
-        ok = mbar_wait(&sm.q_full[nk & 3], (nk >> 2) & 1, abort_flag);
+        ok = mbar_wait_fast(&sm.q_full[nk & 3], (nk >> 2) & 1, abort_flag);
         qf_h = sm.qf[nk & 3][group * kHG + h];
         frame[h] = make_float4(qf_h, 0.f, 0.f, 0.f);
       }
-      ok = ok && mbar_wait(&sm.s_full[b], (g >> 1) & 1, abort_flag);
-      ok = ok && mbar_wait(&sm.full[b][4], (g >> 1) & 1, abort_flag);  // complete already: this thread reads the scales
-      if (ok && g >= 2) ok = mbar_wait(&sm.pv_done[b][3], ((g >> 1) - 1) & 1, abort_flag);  // P's buffer
+      ok = ok && mbar_wait_fast(&sm.s_full[b], (g >> 1) & 1, abort_flag);
+      ok = ok && mbar_wait_fast(&sm.full[b][4], (g >> 1) & 1, abort_flag);  // complete already: this thread reads the scales
+      if (ok && g >= 2) ok = mbar_wait_fast(&sm.pv_done[b][3], ((g >> 1) - 1) & 1, abort_flag);  // P's buffer
       __syncwarp();
       tc_fence_after();
       const uint32_t s_addr = tmem + lanes + b * 64;
@@ -646,7 +646,7 @@ __device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& s
         }
         // O so far moves to the new frames, once its last product is complete.
         if (t > t0 && __any_sync(0xffffffffu, of != 1.f)) {
-          mbar_wait(&sm.pv_done[b ^ 1][3], ((g - 1) >> 1) & 1, abort_flag);
+          mbar_wait_fast(&sm.pv_done[b ^ 1][3], ((g - 1) >> 1) & 1, abort_flag);
           __syncwarp();
           tc_fence_after();
 #pragma unroll 1
