@@ -484,8 +484,8 @@ LSA_API lsa_status lsa_forward(const lsa_config* cfg, int32_t mode, int32_t n_ro
  * block_table int32 [n_seq, max_pages]: token t of sequence b lives in page
  *   block_table[b, t / 64] at row t % 64. Latent and key pages of one layer (and
  *   of every layer that shares the table) use the same page numbers.
- * Slot of a token: page * 64 + row. Pools are limited to n_pages <= 2^25 - 1.
- * Pools must be 16-byte aligned.
+ * Slot of a token: page * 64 + row. Pools are limited to n_pages <= 2^25 - 1, and
+ * max_len to 2^31 - 1. Pools, queries and weights must be 16-byte aligned.
  *
  * Rows (queries): seq_of_row int32 [n_rows] (NULL: row r is sequence r) and pos
  * int32 [n_rows]; a row sees keys 0..pos of its sequence. seq_of_row[r] = -1 marks

@@ -55,6 +55,8 @@ struct Fp8IndexArgs {
   void* ws;        // fp8_index_ws_bytes, 256-byte aligned
 };
 size_t fp8_index_ws_bytes(int n_rows, int n_seq);
+// Whether these rows take the streaming form, which builds histograms on the way.
+bool fp8_index_streams(int n_rows, int n_seq);
 cudaError_t launch_fp8_index(const Fp8IndexArgs& a, cudaStream_t st);
 
 struct Fp8MlaArgs {

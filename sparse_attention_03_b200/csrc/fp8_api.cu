@@ -27,7 +27,7 @@ ForwardPlan forward_plan(const lsa_config* c, int R, int n_seq, int64_t max_len)
   p.hist = take((size_t)R * kTopkHistStride * sizeof(uint32_t));
   p.idx = take((size_t)R * c->index_topk * sizeof(int32_t));
   p.count = take((size_t)R * sizeof(int32_t));
-  p.index = take(fp8_index_ws_bytes(R, n_seq));
+  p.index = take(fp8_index_ws_bytes(R, 1));  // the larger form: a block may hold rows of few sequences
   p.topk_bytes = topk_ws(R, max_len);
   p.topk = take(p.topk_bytes);
   p.mla_bytes = fp8_mla_ws_bytes(R, c->cli_factor, c->index_topk);
@@ -42,7 +42,7 @@ lsa_status check_rows(const char* fn, int32_t n_rows, int32_t n_seq, const int32
     return set_error(LSA_ERR_INVALID, "%s: need n_rows >= 0, n_seq >= 1, max_pages >= 1, max_len >= 1", fn);
   if (n_pages < 1 || n_pages > kMaxPages)
     return set_error(LSA_ERR_INVALID, "%s: need 1 <= n_pages <= %d", fn, kMaxPages);
-  if (max_len > (int64_t)1 << 31) return set_error(LSA_ERR_INVALID, "%s: max_len exceeds 2^31", fn);
+  if (max_len > INT32_MAX) return set_error(LSA_ERR_INVALID, "%s: max_len exceeds 2^31 - 1", fn);
   if (!seq_of_row && n_rows > n_seq)
     return set_error(LSA_ERR_INVALID, "%s: seq_of_row is NULL with more rows than sequences", fn);
   return LSA_OK;
@@ -282,13 +282,18 @@ lsa_status lsa_fp8_forward(const lsa_config* c, int32_t n_rows, int32_t n_seq, c
     a.topk = c->index_topk;
     a.scores = reinterpret_cast<float*>(base + p.scores);
     a.ld = max_len;
-    a.hist = nullptr;
+    // The streaming indexer builds the top-k's histogram from the scores in registers;
+    // rows short enough that the top-k holds all their scores gain nothing from it.
+    const bool hist = fp8_index_streams(nr, rows.n_seq) &&
+                      max_len - c->index_init_tokens - c->index_local_tokens > kTopkShortMid;
+    a.hist = hist ? reinterpret_cast<uint32_t*>(base + p.hist) : nullptr;
     a.ws = base + p.index;
     s = cuda_status(launch_fp8_index(a, st), fn);
     if (s != LSA_OK) return s;
     int32_t* idx = idx_out ? idx_out + (int64_t)r0 * c->index_topk : reinterpret_cast<int32_t*>(base + p.idx);
     int32_t* count = count_out ? count_out + r0 : reinterpret_cast<int32_t*>(base + p.count);
-    s = run_topk(c, nr, rows.pos, max_len, a.scores, max_len, idx, count, base + p.topk, p.topk_bytes, st);
+    s = run_topk(c, nr, rows.pos, max_len, a.scores, max_len, idx, count, base + p.topk, p.topk_bytes, st,
+                 a.hist);
     if (s != LSA_OK) return s;
     Fp8MlaArgs m = {};
     m.rows = rows;

@@ -141,55 +141,104 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PagePlanArgs a)
   }
 }
 
-// One warp quantises one vector of N bf16 (N a multiple of 8): 16-byte chunks
-// lane, lane + 32, ...; the largest magnitude by a warp reduction on the bit
-// patterns, then one multiply and one conversion per element. Returns the scale,
-// and the bits 1 for a vector of zeros.
+// A warp quantises four vectors of N bf16 at once: their 4 N / 8 chunks of 16
+// bytes go round the lanes (288 chunks of a latent: nine full loads a lane, all in
+// flight; one row a warp leaves the third of three loads three quarters idle).
+// Largest magnitudes on the bit patterns, then a multiply and a conversion per element.
+constexpr int kRowsPerWarp = 4;
+
 template <int N>
-__device__ __forceinline__ float2 quant_row(const uint16_t* __restrict__ src, uint8_t* dst, int lane) {
-  constexpr int kChunks = N / 8, kPer = (kChunks + 31) / 32;
-  uint4 v[kPer];
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int c = lane + 32 * i;
-    v[i] = c < kChunks ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
-    m = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(m, v[i].x), v[i].y), v[i].z), v[i].w);
-  }
-  m = fold_max(m);
-  const bool fin = bf16_finite(m);
-  const int e = fin ? scale_exponent(m) : 0;
-  const float inv = pow2i(-e);
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int c = lane + 32 * i;
-    if (c < kChunks) *reinterpret_cast<uint2*>(dst + 8 * c) = fin ? quant8(v[i], inv) : make_uint2(0, 0);
-  }
-  return make_float2(fin ? pow2i(e) : __uint_as_float(0x7fc00000u), __uint_as_float(m == 0 ? 1u : 0u));
-}
+struct Quant4 {
+  static constexpr int kRowChunks = N / 8, kLoads = kRowsPerWarp * kRowChunks / 32;
+  static_assert(kRowsPerWarp * kRowChunks % 32 == 0, "whole loads");
+  uint4 v[kLoads];
+  int e[kRowsPerWarp];       // scale exponents
+  uint32_t m[kRowsPerWarp];  // largest magnitudes (bf16 bits)
 
-constexpr int kAppendWarps = 8;
+  // rows: bit r set where row r is there
+  __device__ __forceinline__ void load(const uint16_t* __restrict__ src, int64_t ld, uint32_t rows, int lane) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int c = lane + 32 * i, r = c / kRowChunks;
+      v[i] = rows >> r & 1 ? __ldg(reinterpret_cast<const uint4*>(src + r * ld) + (c - r * kRowChunks)) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int r = 0; r < kRowsPerWarp; ++r) m[r] = 0;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const uint32_t x = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(0, v[i].x), v[i].y), v[i].z), v[i].w);
+#pragma unroll
+      for (int r = 0; r < kRowsPerWarp; ++r)
+        if (r >= 32 * i / kRowChunks && r <= (32 * i + 31) / kRowChunks)  // the rows that this load touches
+          m[r] = __vmaxu2(m[r], (lane + 32 * i) / kRowChunks == r ? x : 0);
+    }
+#pragma unroll
+    for (int r = 0; r < kRowsPerWarp; ++r) {
+      m[r] = fold_max(m[r]);
+      e[r] = bf16_finite(m[r]) ? scale_exponent(m[r]) : 0;
+    }
+  }
+  // The row's scale (NaN for one with an infinity or NaN, whose codes are zeros).
+  __device__ __forceinline__ float scale(int r) const { return bf16_finite(m[r]) ? pow2i(e[r]) : __uint_as_float(0x7fc00000u); }
+  template <typename F>
+  __device__ __forceinline__ void store(uint32_t rows, int lane, F row_codes) const {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int c = lane + 32 * i, r = c / kRowChunks;
+      int er = 0;
+      bool fin = true;
+#pragma unroll
+      for (int k = 0; k < kRowsPerWarp; ++k)
+        if (k >= 32 * i / kRowChunks && k <= (32 * i + 31) / kRowChunks && k == r) {
+          er = e[k];
+          fin = bf16_finite(m[k]);
+        }
+      if (rows >> r & 1)
+        *reinterpret_cast<uint2*>(row_codes(r) + 8 * (c - r * kRowChunks)) = fin ? quant8(v[i], pow2i(-er)) : make_uint2(0, 0);
+    }
+  }
+};
 
-// Grid y: the arrays of the call (latent sub-blocks, index keys); a warp per row.
+constexpr int kAppendWarps = 4;
+
+// Grid y: the arrays of the call (latent sub-blocks, index keys); four rows a warp.
 __global__ void __launch_bounds__(kAppendWarps * 32) fp8_append_kernel(Fp8AppendArgs a) {
   pdl_wait();
   const int lane = threadIdx.x & 31, y = blockIdx.y;
-  const int64_t r = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
-  if (r >= a.n_rows || !a.src[y]) return;
-  const int slot = a.slot[r];
-  if (slot == -1) return;
-  if (slot < 0 || slot >= (int64_t)a.n_pages * kPage) {
-    if (lane == 0) flag_error(a.err, LSA_DEVERR_PAGE);
-    return;
+  const int64_t r0 = ((int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5)) * kRowsPerWarp;
+  if (r0 >= a.n_rows || !a.src[y]) return;
+  int slot = -1;  // lane r < 4: row r0 + r's
+  if (lane < kRowsPerWarp && r0 + lane < a.n_rows) {
+    slot = a.slot[r0 + lane];
+    if (slot < -1 || slot >= (int64_t)a.n_pages * kPage) {
+      flag_error(a.err, LSA_DEVERR_PAGE);
+      slot = -1;
+    }
   }
+  const uint32_t rows = __ballot_sync(0xffffffffu, slot >= 0);
+  if (rows == 0) return;
+  int at[kRowsPerWarp];
+#pragma unroll
+  for (int r = 0; r < kRowsPerWarp; ++r) at[r] = __shfl_sync(0xffffffffu, slot, r);
+  auto slot_of = [&](int r) { return r == 0 ? at[0] : r == 1 ? at[1] : r == 2 ? at[2] : at[3]; };
   if (y < 2) {
-    uint8_t* dst = a.dst[y] + (int64_t)slot * kLatRow;
-    const float2 s = quant_row<kDLat>(a.src[y] + r * a.ld[y], dst, lane);
-    if (lane == 0) *reinterpret_cast<uint4*>(dst + kDLat) = make_uint4(__float_as_uint(s.x), __float_as_uint(s.y), 0, 0);
+    Quant4<kDLat> q;
+    q.load(a.src[y] + r0 * a.ld[y], a.ld[y], rows, lane);
+    auto row = [&](int r) { return a.dst[y] + (int64_t)slot_of(r) * kLatRow; };
+    q.store(rows, lane, row);
+#pragma unroll
+    for (int r = 0; r < kRowsPerWarp; ++r)
+      if (lane == r && (rows >> r & 1))
+        *reinterpret_cast<uint4*>(row(r) + kDLat) = make_uint4(__float_as_uint(q.scale(r)), q.m[r] == 0 ? 1u : 0u, 0, 0);
   } else {
-    uint8_t* page = a.dst[2] + (int64_t)(slot / kPage) * kKeyPage;
-    const float s = quant_row<kDi>(a.src[2] + r * a.ld[2], page + (slot % kPage) * kDi, lane).x;
-    if (lane == 0) *reinterpret_cast<float*>(page + kPage * kDi + 4 * (slot % kPage)) = s;
+    Quant4<kDi> q;
+    q.load(a.src[2] + r0 * a.ld[2], a.ld[2], rows, lane);
+    auto page = [&](int r) { return a.dst[2] + (int64_t)(slot_of(r) / kPage) * kKeyPage; };
+    q.store(rows, lane, [&](int r) { return page(r) + (slot_of(r) % kPage) * kDi; });
+#pragma unroll
+    for (int r = 0; r < kRowsPerWarp; ++r)
+      if (lane == r && (rows >> r & 1))
+        *reinterpret_cast<float*>(page(r) + kPage * kDi + 4 * (slot_of(r) % kPage)) = q.scale(r);
   }
 }
 
@@ -215,7 +264,8 @@ cudaError_t launch_page_plan(const PagePlanArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_fp8_append(const Fp8AppendArgs& a, cudaStream_t st) {
-  const unsigned nx = (unsigned)((a.n_rows + kAppendWarps - 1) / kAppendWarps);
+  constexpr int kRowsPerCta = kAppendWarps * kRowsPerWarp;
+  const unsigned nx = (unsigned)(((int64_t)a.n_rows + kRowsPerCta - 1) / kRowsPerCta);
   const cudaError_t e = launch_pdl(fp8_append_kernel, dim3(nx, 3), dim3(kAppendWarps * 32), 0, st, a);
   count_launches(1);
   return e;

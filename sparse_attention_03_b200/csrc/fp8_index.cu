@@ -840,6 +840,8 @@ size_t fp8_index_ws_bytes(int n_rows, int n_seq) {
   return use_blocks(n_rows, n_seq) ? (size_t)n_rows * kHi * (kDi + sizeof(float)) : 0;
 }
 
+bool fp8_index_streams(int n_rows, int n_seq) { return !use_blocks(n_rows, n_seq); }
+
 cudaError_t launch_fp8_index(const Fp8IndexArgs& a, cudaStream_t st) {
   CUtensorMap map;
   if (!page_map(&map, a.key_pages, a.rows.n_pages)) return cudaErrorInvalidValue;

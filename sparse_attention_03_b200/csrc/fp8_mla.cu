@@ -470,7 +470,8 @@ __device__ __forceinline__ void mma_role(const Fp8MlaArgs& a, const Split& sp, F
   // O: tile gp, tile tp of item kp
   uint32_t gp = 0, kp = 0;
   int tp = 0;
-  long long t0 = global_ns();
+  uint32_t idle = 0;    // polls in a row that found nothing to issue
+  long long t0 = 0;     // when a long idle stretch began (the timer's read takes as long as a product)
   while (s_live || gp < gs) {
     if (gp < gs) {
       const int b = gp & 1;
@@ -497,15 +498,15 @@ __device__ __forceinline__ void mma_role(const Fp8MlaArgs& a, const Split& sp, F
         } else {
           ++tp;
         }
-        t0 = global_ns();
+        idle = 0;
         continue;
       }
     }
     if (s_live) {
       const int b = gs & 1;
-      // the last chunk's arrivals come after those of the tile's others
-      if (ready(&sm.full[b][3], (gs >> 1) & 1) && (gs < 2 || ready(&sm.s_empty[b], ((gs >> 1) - 1) & 1)) &&
-          (ts > 0 || ready(&sm.q_full[ks & 3], (ks >> 2) & 1))) {
+      // The last chunk's arrivals come after those of the tile's others, and after the
+      // products of tile gs - 2, so after its softmax: S's columns are free too.
+      if (ready(&sm.full[b][3], (gs >> 1) & 1) && (ts > 0 || ready(&sm.q_full[ks & 3], (ks >> 2) & 1))) {
         fence_proxy_async();  // the tile came through cp.async (generic proxy)
         tc_fence_after();
         const uint64_t ad = sw128_desc(k_addr + b * kStageBytes), bd = sw128_desc(q_addr);
@@ -526,14 +527,18 @@ __device__ __forceinline__ void mma_role(const Fp8MlaArgs& a, const Split& sp, F
           ++ks;
           s_live = next_item();
         }
-        t0 = global_ns();
+        idle = 0;
         continue;
       }
     }
-    if (*abort_flag) return;
-    if (global_ns() - t0 > kWaitLimitNs) {
-      *abort_flag = 1;
-      return;
+    if ((++idle & 1023) == 0) {
+      if (*abort_flag) return;
+      const long long t = global_ns();
+      if (idle == 1024) t0 = t;
+      if (t - t0 > kWaitLimitNs) {
+        *abort_flag = 1;
+        return;
+      }
     }
   }
 }

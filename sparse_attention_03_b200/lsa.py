@@ -411,6 +411,18 @@ def _i32(**ts):
         _dt(t, torch.int32, name)
 
 
+def _here(*ts):
+    """The calls run on the current device's stream: every tensor must live there."""
+    dev = None
+    for t in ts:
+        if t is None or not t.is_cuda:
+            continue  # (a host tensor is refused where its pointer is taken)
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if t.device.index != dev:
+            raise ValueError(f"a tensor is on cuda:{t.device.index}, the current device is cuda:{dev}")
+
+
 def _len(t, n, name):
     if t is not None and t.numel() != n:
         raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
@@ -457,6 +469,7 @@ def page_plan(cached, fresh, free_pages, block_table, seq_of_row, pos, slot, tot
     tokens become rows (seq_of_row, pos, slot; -1 behind the last). totals: [rows, pages]."""
     _i32(cached=cached, fresh=fresh, free_pages=free_pages, block_table=block_table, seq_of_row=seq_of_row, pos=pos,
          slot=slot, totals=totals)
+    _here(cached, fresh, free_pages, block_table, seq_of_row, pos, slot, totals)
     n, cap = cached.numel(), seq_of_row.numel()
     _len(fresh, n, "fresh"); _len(pos, cap, "pos"); _len(slot, cap, "slot"); _len(totals, 2, "totals")
     if block_table.dim() != 2 or block_table.shape[0] != n:
@@ -471,6 +484,7 @@ def fp8_append(cfg, slot, latent, latent_pages, k_idx=None, key_pages=None, stre
     [n, 576]) into latent_pages, k_idx (bf16 [n, 128], or None) into key_pages.
     Rows may be a stride apart; slot -1 skips a row."""
     _i32(slot=slot)
+    _here(slot, *latent, *latent_pages, k_idx, key_pages)
     if len(latent) != len(latent_pages):
         raise ValueError("latent and latent_pages must have one entry per sub-block")
     for t in list(latent) + ([] if k_idx is None else [k_idx]):
@@ -501,6 +515,7 @@ def fp8_index_scores(cfg, seq_of_row, pos, q_idx, w, key_pages, block_table, max
     sequence r; -1: a padding row, skipped)."""
     _check_rows(seq_of_row, pos, block_table)
     _dt(q_idx, torch.bfloat16, "q_idx"); _dt(w, torch.float32, "w"); _dt(scores, torch.float32, "scores")
+    _here(seq_of_row, pos, q_idx, w, key_pages, block_table, scores, ws, topk_hist)
     n = pos.numel()
     _len(q_idx, n * 32 * 128, "q_idx"); _len(w, n * 32, "w"); _len(topk_hist, n * TOPK_HIST_WORDS, "topk_hist")
     if scores.dim() != 2 or scores.shape[0] != n:
@@ -533,6 +548,7 @@ def fp8_sparse_mla(cfg, seq_of_row, pos, q_abs, latent_pages, block_table, idx, 
     entries may be None). idx None: every visible key."""
     _check_rows(seq_of_row, pos, block_table)
     _i32(idx=idx, count=count)
+    _here(seq_of_row, pos, *q_abs, *latent_pages, block_table, idx, count, *out, *(lse or []), ws)
     n = pos.numel()
     _len(idx, n * cfg.index_topk, "idx"); _len(count, n, "count")
     k, n_pages, keep = _sub_blocks(cfg, n, q_abs, latent_pages, out, lse)
@@ -549,6 +565,8 @@ def fp8_forward(cfg, seq_of_row, pos, max_len, q_idx, w, key_pages, q_abs, laten
     _check_rows(seq_of_row, pos, block_table)
     _i32(idx_out=idx_out, count_out=count_out)
     _dt(q_idx, torch.bfloat16, "q_idx"); _dt(w, torch.float32, "w")
+    _here(seq_of_row, pos, q_idx, w, key_pages, *q_abs, *latent_pages, block_table, *out, *(lse or []), ws, idx_out,
+          count_out)
     n = pos.numel()
     _len(q_idx, n * 32 * 128, "q_idx"); _len(w, n * 32, "w")
     _len(idx_out, n * cfg.index_topk, "idx_out"); _len(count_out, n, "count_out")
