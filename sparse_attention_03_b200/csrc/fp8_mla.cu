@@ -34,10 +34,10 @@
 // twice 64 columns, O 4 x 64.
 //
 // Roles (16 warps, one CTA per SM, persistent over (row, sub-block, split)
-// items): 8 softmax warps (a thread = a key of the tile and 16 heads), 7 gather warps (16-byte
-// cp.async into the swizzled layout, a ring of two tiles that is refilled chunk
-// by chunk; between tiles the next item's query codes and, the first four, an
-// item's O when its last product is complete), and one MMA warp
+// items): 8 softmax warps (a thread = a key of the tile and 16 heads; between
+// items the next query's codes), 7 gather warps (16-byte cp.async into the
+// swizzled layout, a ring of two tiles that is refilled chunk by chunk; the first
+// four also write an item's O when its last product is complete), and one MMA warp
 // that issues what is ready, so that the softmax of a tile runs under the
 // products of its neighbours. Every wait is bounded.
 #include "fp8.cuh"
@@ -78,7 +78,7 @@ struct __align__(1024) Fp8MlaSmem {
   float fin_m[4][kH];
   // per stage and chunk: gathered; read by its products (chunk 4, which has none: s_empty)
   uint64_t full[2][kChunks], pv_done[2][4];
-  uint64_t s_full[2], s_empty[2], p_full[2], q_full[4], fin_full[4], q_empty, o_full, o_empty, drain;
+  uint64_t s_full[2], s_empty[2], p_full[2], q_full[4], fin_full[4], o_full, o_empty, drain;
   int item_tiles[4];                   // ring over items, of the MMA warp
   uint32_t tmem_base;
   int abort_flag;
@@ -177,31 +177,35 @@ __device__ __forceinline__ bool softmax_any(int group, bool v) {
 
 // ---------------------------------------------------------------- query codes
 
-// Gather warp w quantises heads w, w + 7, .. of an item's query, once the
-// previous item's last S is complete. A loop over the heads, the next one's
-// loads in flight: the code runs once an item, so that its size counts.
-__device__ __forceinline__ void load_head(const uint4* src, int h, int lane, uint4 (&v)[3]) {
-#pragma unroll
-  for (int c = 0; c < 3; ++c)
-    v[c] = h < kH && lane + 32 * c < 72 ? __ldg(src + h * 72 + lane + 32 * c) : make_uint4(0, 0, 0, 0);
+// Softmax warp w quantises heads 4 w .. 4 w + 3 of an item's query, when the
+// previous item's last S is complete (the warp has read it). All loads first.
+constexpr int kQHeads = kH / kSoftWarps;
+
+__device__ __forceinline__ const uint4* query_of(const Fp8MlaArgs& a, const Split& sp, int item, int warp) {
+  return reinterpret_cast<const uint4*>(a.q[item_sub(a, sp, item)] + (int64_t)item_row(a, sp, item) * kH * kDLat) +
+         warp * kQHeads * 72;
+}
+// Brings the warp's heads of a query to the L2 cache: 36 lines.
+__device__ __forceinline__ void prefetch_q(const uint4* src, int lane) {
+  asm volatile("prefetch.global.L2 [%0];\n" ::"l"(src + lane * 8));
+  if (lane < 4) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(src + (32 + lane) * 8));
 }
 
-__device__ __forceinline__ void prepare_q(const Fp8MlaArgs& a, const Split& sp, Fp8MlaSmem& sm, int item, uint32_t nk,
-                                          int warp, int lane) {
-  const uint4* src =
-      reinterpret_cast<const uint4*>(a.q[item_sub(a, sp, item)] + (int64_t)item_row(a, sp, item) * kH * kDLat);
-  uint4 next[3];
-  load_head(src, warp, lane, next);
-#pragma unroll 1
-  for (int h = warp; h < kH; h += kGatherWarps) {
-    uint4 v[3];
+__device__ __forceinline__ void prepare_q(const Fp8MlaArgs& a, Fp8MlaSmem& sm, const uint4* src, uint32_t nk, int warp,
+                                          int lane) {
+  uint4 v[kQHeads][3];
+#pragma unroll
+  for (int j = 0; j < kQHeads; ++j)
+#pragma unroll
+    for (int c = 0; c < 3; ++c)
+      v[j][c] = lane + 32 * c < 72 ? __ldg(src + j * 72 + lane + 32 * c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int j = 0; j < kQHeads; ++j) {
+    const int h = warp * kQHeads + j;
     uint32_t m = 0;
 #pragma unroll
-    for (int c = 0; c < 3; ++c) {
-      v[c] = next[c];
-      m = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(m, v[c].x), v[c].y), v[c].z), v[c].w);
-    }
-    load_head(src, h + kGatherWarps, lane, next);
+    for (int c = 0; c < 3; ++c)
+      m = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(m, v[j][c].x), v[j][c].y), v[j][c].z), v[j][c].w);
     m = fold_max(m);
     const bool fin = bf16_finite(m);
     const int e = fin ? scale_exponent(m) : 0;
@@ -209,7 +213,7 @@ __device__ __forceinline__ void prepare_q(const Fp8MlaArgs& a, const Split& sp, 
 #pragma unroll
     for (int c = 0; c < 3; ++c) {
       const int u = lane + 32 * c;  // eight elements
-      const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+      const uint32_t w[4] = {v[j][c].x, v[j][c].y, v[j][c].z, v[j][c].w};
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k)  // 8 significant bits fit fp16; what is below 2^-24 of the largest goes
@@ -334,9 +338,9 @@ __device__ __forceinline__ void gather_role(const Fp8MlaArgs& a, const Split& sp
     int page;
     bool there;
   };
-  struct Tag {  // a tile's item (-1: none), whether it is its first and its last
+  struct Tag {  // a tile's item (-1: none), whether it is its last
     int item;
-    bool first, last;
+    bool last;
   };
   auto entry_of = [&](const TileCursor& c) {
     Entry e = {(uint32_t)c.t * kTile + key_t, c.it.nvis, c.it.seq, false};
@@ -354,7 +358,7 @@ __device__ __forceinline__ void gather_role(const Fp8MlaArgs& a, const Split& sp
     return r;
   };
   auto tag_of = [&](const TileCursor& c) {
-    return c.i < sp.n_items ? Tag{c.i, c.t == c.it.t0, c.t + 1 == c.it.t1} : Tag{-1, false, false};
+    return c.i < sp.n_items ? Tag{c.i, c.t + 1 == c.it.t1} : Tag{-1, false};
   };
   TileCursor ahead;
   ahead.start(a, sp, blockIdx.x, report);
@@ -394,11 +398,6 @@ __device__ __forceinline__ void gather_role(const Fp8MlaArgs& a, const Split& sp
                      lat + (int64_t)max(at[j], 0) * kLatRow + c * 128, at[j] >= 0 ? 16 : 0);
       }
       cp_async_arrive(&sm.full[b][c]);
-    }
-    if (cur.first) {
-      if (nk > 0 && !mbar_wait_fast(&sm.q_empty, (nk - 1) & 1, abort_flag)) return;
-      __syncwarp();
-      prepare_q(a, sp, sm, cur.item, nk, warp, lane);
     }
     // The item that ended two tiles ago is complete (this tile is in its places): its O.
     if (warp < 4 && older.item >= 0 && older.last_g + 2 == g) {
@@ -517,10 +516,7 @@ __device__ __forceinline__ void mma_role(const Fp8MlaArgs& a, const Split& sp, F
           umma_f8(tmem + b * 64, ad + ((c * kChunkBytes + o) >> 4), bd + ((c * kQChunkBytes + o) >> 4), id,
                   k > 0 ? 1u : 0u, leader);
         }
-        if (leader) {
-          umma_commit(&sm.s_full[b]);
-          if (ts + 1 == ts1) umma_commit(&sm.q_empty);
-        }
+        if (leader) umma_commit(&sm.s_full[b]);
         __syncwarp();
         ++gs;
         if (++ts == ts1) {
@@ -575,10 +571,21 @@ __device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& s
   float4* frame = sm.frame[warp];
   float2* move = sm.move[warp];
   uint32_t g = 0, nk = 0;
-  for (int i = blockIdx.x; i < sp.n_items; i += gridDim.x) {
-    const Item it = load_item(a, sp, i, false);
-    const int t0 = it.t0, t1 = it.t1;
-    if (t0 >= t1) continue;
+  // The next item from `i` on that has tiles.
+  int i = blockIdx.x, t0 = 0, t1 = 0;
+  auto find = [&]() {
+    for (; i < sp.n_items; i += gridDim.x) {
+      const Item it = load_item(a, sp, i, false);
+      t0 = it.t0;
+      t1 = it.t1;
+      if (t0 < t1) break;
+    }
+  };
+  if (i < sp.n_items) prefetch_q(query_of(a, sp, i, warp), lane);
+  find();
+  if (i < sp.n_items) prepare_q(a, sm, query_of(a, sp, i, warp), nk, warp, lane);
+  while (i < sp.n_items) {
+    if (i + (int)gridDim.x < sp.n_items) prefetch_q(query_of(a, sp, i + gridDim.x, warp), lane);
     float L[kHG];
 #pragma unroll
     for (int j = 0; j < kHG; ++j) L[j] = 0.f;
@@ -702,6 +709,9 @@ __device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& s
       if (lane == 0) mbar_arrive(&sm.fin_full[f]);
     }
     ++nk;
+    i += gridDim.x;
+    find();
+    if (i < sp.n_items) prepare_q(a, sm, query_of(a, sp, i, warp), nk, warp, lane);
   }
 }
 
@@ -724,10 +734,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.p_full[b], kSoftWarps);
     }
     for (int b = 0; b < 4; ++b) {
-      mbar_init(&sm.q_full[b], kGatherWarps);
+      mbar_init(&sm.q_full[b], kSoftWarps);
       mbar_init(&sm.fin_full[b], 2);
     }
-    mbar_init(&sm.q_empty, 1);
     mbar_init(&sm.o_full, 1);
     mbar_init(&sm.o_empty, 4);
     mbar_init(&sm.drain, 1);
