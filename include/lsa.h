@@ -572,7 +572,8 @@ LSA_API lsa_status lsa_fp8_index_scores(const lsa_config* cfg, int32_t n_rows, i
  * q_abs, latent_pages, out, lse: HOST arrays of n_sub DEVICE pointers (lse, or
  * an entry of it, may be NULL): q_abs bf16 [n_rows, 32, 576], out bf16
  * [n_rows, 32, 512], lse fp32 [n_rows, 32]. The query enters to its last bit
- * (to 2^-22 of its head's largest element); the softmax weights times their
+ * (to 2^-22 of the row's largest element; a query with an
+ * infinity or NaN gives NaN); the softmax weights times their
  * scales are rounded to 8 significant bits, as a bf16 weight is, and lost below
  * 2^-17 of the largest of them. Logits, sums and outputs accumulate in fp32.
  * Workspace optional (split-K partials): lsa_workspace_size(LSA_OP_FP8_MLA).

@@ -12,9 +12,9 @@
 // stand side by side in the N dimension (32 heads hi, 32 heads lo; N = 64 runs
 // at the rate of N = 32, 48 against 45 cycles an instruction, both held by the
 // 4 KB A operand):
-//   - the query, scaled per head by a power of two to at most 448, k = 16: bf16
-//     has 8 significant bits, two e4m3 of 4 bits hold them exactly down to 2^-22
-//     of the head's largest element;
+//   - the query, scaled by a power of two to at most 448, k = 16: bf16 has 8
+//     significant bits, two e4m3 of 4 bits hold them exactly down to 2^-22 of the
+//     row's largest element;
 //   - the weight u = p * s_i * 2^(2 - A), at most 128, k = 64: 8 significant
 //     bits, the precision of a bf16 weight, in steps of at least 2^-15 (2^-16 of
 //     the largest u of its frame: what is below is lost).
@@ -69,11 +69,10 @@ struct __align__(1024) Fp8MlaSmem {
   uint8_t k[2][kStageBytes];
   uint8_t q[kChunks * kQChunkBytes];   // [chunk][32 hi rows, 32 lo rows][128 B]
   uint8_t p[2][kPBytes];               // [key][32 hi, 32 lo codes]
-  float4 frame[kSoftWarps][kHG];       // per softmax warp: q factor, -m, 2^(2 - A + m)
-  float2 move[kSoftWarps][kHG];        // per softmax warp: factors of L and O
+  float4 frame[kSoftWarps][kHG];       // per softmax warp, new frames: -m, 2^(2 - A + m), factors of L and O
   float2 tmax[kSoftWarps][kHG];        // each warp's maxima of a tile
   float lsum[kSoftWarps][kHG];
-  float qf[4][kH];                     // ring over items: the heads' query factors
+  uint32_t qmax[kSoftWarps];           // each softmax warp's largest magnitude of the query
   float2 fin[4][kH];                   // ring over items: 2^(A - m - 2), the sum of the softmax
   float fin_m[4][kH];
   // per stage and chunk: gathered; read by its products (chunk 4, which has none: s_empty)
@@ -175,6 +174,18 @@ __device__ __forceinline__ bool softmax_any(int group, bool v) {
   return r != 0;
 }
 
+// The same for both groups.
+__device__ __forceinline__ bool all_softmax_any(bool v) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 q, %1, 0;\n bar.red.or.pred p, 3, 256, q;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+
 // ---------------------------------------------------------------- query codes
 
 // Softmax warp w quantises heads 4 w .. 4 w + 3 of an item's query, when the
@@ -191,25 +202,34 @@ __device__ __forceinline__ void prefetch_q(const uint4* src, int lane) {
   if (lane < 4) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(src + (32 + lane) * 8));
 }
 
-__device__ __forceinline__ void prepare_q(const Fp8MlaArgs& a, Fp8MlaSmem& sm, const uint4* src, uint32_t nk, int warp,
-                                          int lane) {
+// Returns the factor of the codes' products: one power of two for all heads of
+// the row (a logit's error counts absolutely) times the softmax's; NaN for a
+// query with an infinity or NaN.
+__device__ __forceinline__ float prepare_q(const Fp8MlaArgs& a, Fp8MlaSmem& sm, const uint4* src, uint32_t nk, int warp,
+                                           int lane) {
   uint4 v[kQHeads][3];
 #pragma unroll
   for (int j = 0; j < kQHeads; ++j)
 #pragma unroll
     for (int c = 0; c < 3; ++c)
       v[j][c] = lane + 32 * c < 72 ? __ldg(src + j * 72 + lane + 32 * c) : make_uint4(0, 0, 0, 0);
+  uint32_t m = 0;
 #pragma unroll
-  for (int j = 0; j < kQHeads; ++j) {
-    const int h = warp * kQHeads + j;
-    uint32_t m = 0;
+  for (int j = 0; j < kQHeads; ++j)
 #pragma unroll
     for (int c = 0; c < 3; ++c)
       m = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(m, v[j][c].x), v[j][c].y), v[j][c].z), v[j][c].w);
-    m = fold_max(m);
-    const bool fin = bf16_finite(m);
-    const int e = fin ? scale_exponent(m) : 0;
-    const float inv = pow2i(-e);
+  m = fold_max(m);
+  if (lane == 0) sm.qmax[warp] = m;
+  all_softmax_any(false);
+#pragma unroll
+  for (int w = 0; w < kSoftWarps; ++w) m = max(m, sm.qmax[w]);
+  const bool fin = bf16_finite(m);
+  const int e = fin ? scale_exponent(m) : 0;
+  const float inv = pow2i(-e);
+#pragma unroll
+  for (int j = 0; j < kQHeads; ++j) {
+    const int h = warp * kQHeads + j;
 #pragma unroll
     for (int c = 0; c < 3; ++c) {
       const int u = lane + 32 * c;  // eight elements
@@ -225,11 +245,11 @@ __device__ __forceinline__ void prepare_q(const Fp8MlaArgs& a, Fp8MlaSmem& sm, c
         *reinterpret_cast<uint2*>(base + 32 * 128) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
       }
     }
-    if (lane == 0) sm.qf[nk & 3][h] = fin ? pow2i(e) * (a.scale * kLog2e) : __uint_as_float(0x7fc00000u);
   }
   fence_proxy_async();
   __syncwarp();
   if (lane == 0) mbar_arrive(&sm.q_full[nk & 3]);
+  return fin ? pow2i(e) * (a.scale * kLog2e) : __uint_as_float(0x7fc00000u);
 }
 
 // ---------------------------------------------------------------- output
@@ -542,17 +562,21 @@ __device__ __forceinline__ void mma_role(const Fp8MlaArgs& a, const Split& sp, F
 // ---------------------------------------------------------------- softmax warps
 
 // The weights of one key (a thread) for the group's 16 heads in the given
-// frames: p for the sum, u = p s 2^(2 - A + m) for the product; S from tensor
-// memory. `su`: the scale, or 0 for a key that adds nothing to O.
-__device__ __forceinline__ void weights(uint32_t s_addr, const float4* frame, bool valid, float s, float su,
+// frames (in registers: a shared load waits behind the gather's copies): p for
+// the sum, u = p s 2^(2 - A + m) for the product; S from tensor memory. `sq`: the
+// key's scale times the query's factor; `su`: the scale, or 0 for a key that adds
+// nothing to O.
+struct Frames {
+  float m[kHG], w[kHG];  // -m, 2^(2 - A + m)
+};
+__device__ __forceinline__ void weights(uint32_t s_addr, const Frames& f, bool valid, float sq, float su,
                                         float (&p)[kHG], float (&u)[kHG], float& top_p, float& top_u) {
   tmem_ld16_x2(s_addr, s_addr + kH, p, u);  // hi and lo
   top_p = top_u = 0.f;
 #pragma unroll
   for (int h = 0; h < kHG; ++h) {
-    const float4 f = frame[h];
-    p[h] = ex2(fmaf(fmaf(u[h], 0.0625f, p[h]) * f.x, s, f.y));
-    u[h] = p[h] * (su * f.z);
+    p[h] = ex2(fmaf(fmaf(u[h], 0.0625f, p[h]), sq, f.m[h]));
+    u[h] = p[h] * (su * f.w[h]);
     top_p = fmaxf(top_p, p[h]);
     top_u = fmaxf(top_u, u[h]);
   }
@@ -569,7 +593,7 @@ __device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& s
   const int key = quarter * 32 + lane, h = lane & 15;  // this lane keeps the frames of the group's head h
   const uint32_t lanes = ((uint32_t)(quarter * 32) << 16) + group * kHG;
   float4* frame = sm.frame[warp];
-  float2* move = sm.move[warp];
+  Frames f;
   uint32_t g = 0, nk = 0;
   // The next item from `i` on that has tiles.
   int i = blockIdx.x, t0 = 0, t1 = 0;
@@ -583,41 +607,37 @@ __device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& s
   };
   if (i < sp.n_items) prefetch_q(query_of(a, sp, i, warp), lane);
   find();
-  if (i < sp.n_items) prepare_q(a, sm, query_of(a, sp, i, warp), nk, warp, lane);
+  float qf = 0.f;  // the query's factor
+  if (i < sp.n_items) qf = prepare_q(a, sm, query_of(a, sp, i, warp), nk, warp, lane);
   while (i < sp.n_items) {
     if (i + (int)gridDim.x < sp.n_items) prefetch_q(query_of(a, sp, i + gridDim.x, warp), lane);
     float L[kHG];
 #pragma unroll
-    for (int j = 0; j < kHG; ++j) L[j] = 0.f;
-    float m_h = 0.f, a_h = kUnset, qf_h = 0.f;  // head h's frames (every warp of the group the same)
-    bool framed = false;
+    for (int j = 0; j < kHG; ++j) L[j] = f.m[j] = f.w[j] = 0.f;
+    float m_h = 0.f, a_h = kUnset;  // head h's frames (every warp of the group the same)
+    bool framed = false, dead = false;
     for (int t = t0; t < t1; ++t, ++g) {
       const int b = g & 1;
-      bool ok = true;
-      if (t == t0) {
-        ok = mbar_wait_fast(&sm.q_full[nk & 3], (nk >> 2) & 1, abort_flag);
-        qf_h = sm.qf[nk & 3][group * kHG + h];
-        frame[h] = make_float4(qf_h, 0.f, 0.f, 0.f);
-      }
-      ok = ok && mbar_wait_fast(&sm.s_full[b], (g >> 1) & 1, abort_flag);
-      ok = ok && mbar_wait_fast(&sm.full[b][4], (g >> 1) & 1, abort_flag);  // complete already: this thread reads the scales
-      if (ok && g >= 2) ok = mbar_wait_fast(&sm.pv_done[b][3], ((g >> 1) - 1) & 1, abort_flag);  // P's buffer
-      __syncwarp();
-      tc_fence_after();
-      const uint32_t s_addr = tmem + lanes + b * 64;
+      // The tile is here (this thread reads its scale), so the products of tile g - 2
+      // are complete: P's buffer is free.
+      bool ok = mbar_wait_fast(&sm.full[b][3], (g >> 1) & 1, abort_flag);
       uint2 tail;
       asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];\n"
                    : "=r"(tail.x), "=r"(tail.y)
                    : "r"(smem_u32(sm.k[b] + 4 * kChunkBytes + key * 128 + ((4 ^ (key & 7)) << 4))));
+      ok = ok && mbar_wait_fast(&sm.s_full[b], (g >> 1) & 1, abort_flag);
+      __syncwarp();
+      tc_fence_after();
+      const uint32_t s_addr = tmem + lanes + b * 64;
       const float s = __uint_as_float(tail.x);
       const bool valid = s != 0.f;                    // a masked key's row is zeros
       const bool silent = !valid || tail.y != 0;      // adds nothing to O
-      const float su = silent ? 0.f : s;
+      const float su = silent ? 0.f : s, sq = s * qf;
       const bool anew = (t - t0) % kFrameTiles == 0;
       float p[kHG], u[kHG], top_p = 0.f, top_u = 0.f;
       bool force = anew || !framed || !ok, moved = false;
       while (true) {
-        if (!force) weights(s_addr, frame, valid, s, su, p, u, top_p, top_u);
+        if (!force) weights(s_addr, f, valid, sq, su, p, u, top_p, top_u);
         if (!softmax_any(group, force || (!moved && (top_u > 128.f || top_p > 0x1p60f)))) break;
         force = false;
         moved = true;
@@ -626,15 +646,15 @@ __device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& s
         tmem_ld16_x2(s_addr, s_addr + kH, p, u);
 #pragma unroll
         for (int j = 0; j < kHG; ++j) {
-          const float4 f = frame[j];
-          p[j] = valid ? fmaf(fmaf(u[j], 0.0625f, p[j]) * f.x, s, f.y) : -INFINITY;
+          p[j] = valid ? fmaf(fmaf(u[j], 0.0625f, p[j]), sq, f.m[j]) : -INFINITY;
         }
         const float e = (float)((int)(tail.x >> 23) - 127);
 #pragma unroll
         for (int j = 0; j < kHG; ++j) u[j] = silent ? -INFINITY : p[j] + e;
         const float tl_w = fold16<true>(p, lane), ta_w = fold16<true>(u, lane);
         sm.tmax[warp][h] = make_float2(tl_w, ta_w);
-        if (softmax_any(group, !ok || *abort_flag)) return;
+        dead = softmax_any(group, !ok || *abort_flag);
+        if (dead) break;
         float tl = -INFINITY, ta = -INFINITY;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -647,14 +667,15 @@ __device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& s
         framed = framed || __any_sync(0xffffffffu, tl > -INFINITY);
         const float of = pow2f(a_old - a_h);
         __syncwarp();
-        frame[h] = make_float4(qf_h, -m_h, pow2f(fminf(2.f - (a_h - m_h), 126.f)), 0.f);
-        move[h] = make_float2(pow2f(m_old - m_h), of);
+        frame[h] = make_float4(-m_h, pow2f(fminf(2.f - (a_h - m_h), 126.f)), pow2f(m_old - m_h), of);
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < kHG; ++j) {
-          const float2 mv = move[j];
-          L[j] *= mv.x;
-          u[j] = mv.y;
+          const float4 fr = frame[j];
+          f.m[j] = fr.x;
+          f.w[j] = fr.y;
+          L[j] *= fr.z;
+          u[j] = fr.w;
         }
         // O so far moves to the new frames, once its last product is complete.
         if (t > t0 && __any_sync(0xffffffffu, of != 1.f)) {
@@ -675,6 +696,7 @@ __device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& s
           }
         }
       }
+      if (dead) break;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.s_empty[b]);  // S and the scales are read
@@ -699,7 +721,7 @@ __device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& s
     }
     // The item's sums, for the output.
     sm.lsum[warp][h] = fold16<false>(L, lane);
-    if (softmax_any(group, *abort_flag != 0)) return;
+    if (all_softmax_any(dead || *abort_flag)) return;  // both groups or neither: they meet at the next query
     if (quarter == 0) {
       const float l = (sm.lsum[w0][h] + sm.lsum[w0 + 1][h]) + (sm.lsum[w0 + 2][h] + sm.lsum[w0 + 3][h]);
       const int f = nk & 3;
@@ -711,7 +733,7 @@ __device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& s
     ++nk;
     i += gridDim.x;
     find();
-    if (i < sp.n_items) prepare_q(a, sm, query_of(a, sp, i, warp), nk, warp, lane);
+    if (i < sp.n_items) qf = prepare_q(a, sm, query_of(a, sp, i, warp), nk, warp, lane);
   }
 }
 
@@ -750,10 +772,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort_flag = &sm.abort_flag;
-  // Registers: 512 threads x 128 at launch; the softmax's two warpgroups take 40 a
-  // thread from the other two (2 x 168 + 2 x 88 = 4 x 128).
-  if (warp < kSoftWarps) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;\n" ::);
-  else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n" ::);
+  // Registers: 512 threads x 128 at launch; the softmax's two warpgroups take 48 a
+  // thread from the other two (2 x 176 + 2 x 80 = 4 x 128).
+  if (warp < kSoftWarps) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;\n" ::);
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n" ::);
   if (warp < kSoftWarps) {
     softmax_role(a, sp, sm, tmem, warp, lane, abort_flag);
   } else if (warp < kMmaWarp) {

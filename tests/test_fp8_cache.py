@@ -304,11 +304,11 @@ def _mla_tol(q, c_val, s, keys, weights, out, scale):
     pieces (2^-8), their smallest step (weight * scale is carried as u = hi + lo / 64 with lo an e4m3 of smallest
     step 2^-9, so u is off by at most 2^-16, and the largest u of a frame is at least 2: 2^-17 of the largest
     weight * scale, times the codes), and the logits' fp32 sums of 576 exact
-    products (a truncated addition loses 2^-23 of the absolute sum) with the query's split (2^-22 of the head's
+    products (a truncated addition loses 2^-23 of the absolute sum) with the query's split (2^-22 of the row's
     largest element): delta, once in a weight and once in the sum."""
     c = c_val[np.asarray(keys)]
     delta = scale * (577 * 2.0 ** -23 * (np.abs(q) @ np.abs(c).T)
-                     + 2.0 ** -22 * np.abs(q).max(1)[:, None] * np.abs(c).sum(1)[None]).max(1) + 2.0 ** -18
+                     + 2.0 ** -22 * np.abs(q).max() * np.abs(c).sum(1)[None]).max(1) + 2.0 ** -18
     v = np.abs(c[:, :512])
     s = np.asarray(s)[np.asarray(keys)]
     s_loud = np.where(c.any(axis=1), s, 0.0)             # a row of zeros has an arbitrary scale, which does not count
