@@ -20,11 +20,11 @@
 //     the largest u of its frame: what is below is lost).
 // The frame A of each head (an integer, so that rescaling is exact) follows the
 // running maximum of log2(p s): it is set from the first tile, raised when a u
-// would pass 128, and set anew every 16 tiles (also downwards: O is then scaled
-// up, fp32 has the range), so that the loss stays relative to the 2048 keys
-// around a key however long the list is. The sum of the softmax is kept apart,
-// in fp32, of the unrounded weights, in its own frame m (a key's scale, which is
-// no part of its weight, cannot disturb it).
+// would pass 128, and set anew every 16 tiles (also downwards, to 2^-60 of the
+// highest: O is then scaled up, fp32 has the range), so that the loss stays
+// relative to the 2048 keys around a key however long the list is. The sum of the
+// softmax is kept apart, in fp32, of the unrounded weights, in its own frame m (a
+// key's scale, which is no part of its weight, cannot disturb it).
 //
 // Layout. One tile is 128 keys: S^T [128 keys x 64] = C Q^T (K = 576: 18
 // instructions), then O^T [512 dims x 64] += C^T P (4 x 4 instructions of 128
@@ -499,7 +499,7 @@ __device__ __forceinline__ void mma_role(const Fp8MlaArgs& a, const Split& sp, F
         const bool last = tp + 1 == sm.item_tiles[kp & 3];
         const uint64_t ad = sw128_mn_desc(k_addr + b * kStageBytes, 1024), bd = sw64_mn_desc(p_addr + b * kPBytes);
         constexpr uint32_t id = f8_idesc(64, true);
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -530,11 +530,12 @@ __device__ __forceinline__ void mma_role(const Fp8MlaArgs& a, const Split& sp, F
         tc_fence_after();
         const uint64_t ad = sw128_desc(k_addr + b * kStageBytes), bd = sw128_desc(q_addr);
         constexpr uint32_t id = f8_idesc(64, false);
-#pragma unroll
-        for (int k = 0; k < 18; ++k) {
+#pragma unroll 1
+        for (int k = 0; k < 18; k += 2) {  // (a short loop: straight code waits for its instructions)
           const uint32_t c = k >> 2, o = (k & 3) * 32;
-          umma_f8(tmem + b * 64, ad + ((c * kChunkBytes + o) >> 4), bd + ((c * kQChunkBytes + o) >> 4), id,
-                  k > 0 ? 1u : 0u, leader);
+          const uint64_t a0 = ad + ((c * kChunkBytes + o) >> 4), b0 = bd + ((c * kQChunkBytes + o) >> 4);
+          umma_f8(tmem + b * 64, a0, b0, id, k > 0 ? 1u : 0u, leader);
+          umma_f8(tmem + b * 64, a0 + 2, b0 + 2, id, 1u, leader);
         }
         if (leader) umma_commit(&sm.s_full[b]);
         __syncwarp();
@@ -614,7 +615,7 @@ __device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& s
     float L[kHG];
 #pragma unroll
     for (int j = 0; j < kHG; ++j) L[j] = f.m[j] = f.w[j] = 0.f;
-    float m_h = 0.f, a_h = kUnset;  // head h's frames (every warp of the group the same)
+    float m_h = 0.f, a_h = kUnset, a_top = kUnset;  // head h's frames (every warp of the group the same)
     bool framed = false, dead = false;
     for (int t = t0; t < t1; ++t, ++g) {
       const int b = g & 1;
@@ -663,7 +664,9 @@ __device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& s
         }
         const float m_old = m_h, a_old = a_h;
         if (tl > -INFINITY) m_h = framed ? fmaxf(m_old, ceilf(tl + m_old)) : ceilf(tl + m_old);
-        if (ta > -INFINITY) a_h = fmaxf(ceilf(ta + m_old), anew ? a_old - 60.f : a_old);
+        // down by at most 2^60 from the item's highest: O, scaled up by as much, stays far from overflow
+        if (ta > -INFINITY) a_h = fmaxf(ceilf(ta + m_old), anew ? a_top - 60.f : a_old);
+        a_top = fmaxf(a_top, a_h);
         framed = framed || __any_sync(0xffffffffu, tl > -INFINITY);
         const float of = pow2f(a_old - a_h);
         __syncwarp();

@@ -506,18 +506,7 @@ def test_scores_decode(lens, hist):
         err, scores, pos, h, _ = _score_case(lens, rows, cfg, hist=hist, ld_extra=3)
         assert err == 0
         if hist:  # the histogram is the top-k's own first pass over these scores
-            for r, (s, p) in enumerate(rows):
-                bins = h[r, :2048].cpu().numpy()
-                lo, hi = cfg.index_init_tokens, p + 1 - cfg.index_local_tokens
-                want = np.zeros(2048, dtype=np.int64)
-                if p + 1 > cfg.index_topk and hi > lo:
-                    f = scores[r, lo:hi].cpu().numpy().copy()
-                    f[f == 0] = 0.0
-                    u = f.view(np.uint32)
-                    key = np.where(u & 0x80000000, ~u, u | 0x80000000)
-                    np.add.at(want, key >> 21, 1)
-                np.testing.assert_array_equal(bins, want)
-                assert not h[r, 2048:].cpu().numpy().any()
+            _check_hist(rows, scores, h, cfg)
 
 
 @gpu
@@ -535,6 +524,45 @@ def test_scores_rows_of_prompts(lens, new, pad):
     for cfg in (lsa.LsaConfig(**TINY), lsa.LsaConfig(index_topk=64, index_init_tokens=0, index_local_tokens=0)):
         err, *_ = _score_case(lens, rows, cfg, seed=len(lens), max_len=max(lens) + 11)
         assert err == 0
+
+
+def _check_hist(rows, scores, h, cfg):
+    for r, (s, p) in enumerate(rows):
+        lo, hi = cfg.index_init_tokens, p + 1 - cfg.index_local_tokens
+        want = np.zeros(2048, dtype=np.int64)
+        if s >= 0 and p + 1 > cfg.index_topk and hi > lo:
+            f = scores[r, lo:hi].cpu().numpy().copy()
+            f[f == 0] = 0.0
+            u = f.view(np.uint32)
+            np.add.at(want, np.where(u & 0x80000000, ~u, u | 0x80000000) >> 21, 1)
+        np.testing.assert_array_equal(h[r, :2048].cpu().numpy(), want)
+        assert not h[r, 2048:].cpu().numpy().any()
+
+
+@gpu
+def test_scores_of_prompt_rows_with_the_histogram():
+    lens = [300, 150]
+    rows = [(s, p) for s, n in enumerate(lens) for p in range(n - 40, n)]
+    cfg = lsa.LsaConfig(**TINY)
+    err, scores, pos, h, _ = _score_case(lens, rows, cfg, hist=True)
+    assert err == 0
+    _check_hist(rows, scores, h, cfg)
+
+
+@gpu
+@pytest.mark.parametrize("hist", [False, True])
+def test_scores_of_many_short_sequences(hist):
+    # more rows than the GPU runs CTAs of the streaming form: each takes the tiles of several rows
+    rng = np.random.default_rng(8)
+    lens = rng.integers(1, 300, 500).tolist()
+    rows = [(s, n - 1) for s, n in enumerate(lens)]
+    for i in (0, 17, 18, 499):
+        rows[i] = (-1, -1)
+    cfg = lsa.LsaConfig(**TINY)
+    err, scores, pos, h, _ = _score_case(lens, rows, cfg, hist=hist)
+    assert err == 0
+    if hist:
+        _check_hist(rows, scores, h, cfg)
 
 
 @gpu
@@ -648,6 +676,51 @@ def test_mla_dense_beyond_the_selection_size():
     _mla_case(c, [(0, 4999)], None, cfg)
     _mla_case(c, [(0, 4999)], None, cfg, ws=None)
     _mla_case(c, [(0, 4999), (0, 3), (0, 2500)], None, cfg)
+
+
+@gpu
+@pytest.mark.parametrize("first", [6.0, 60.0])
+def test_mla_dense_with_the_weight_in_front(first):
+    # the first keys outweigh every later one: the weights' frame comes down again every 16 tiles
+    rng = np.random.default_rng(19)
+    n = 4500
+    q = _bf16(rng.standard_normal((1, 32, 576))).cuda()
+    x = rng.standard_normal((n, 576)) * 0.05
+    mean = _vals(q)[0].mean(0)
+    x[:3] = mean / (mean @ mean) * first * 192 ** 0.5
+    lat = _bf16(x).cuda()
+    c = Caches([n], 20, cli=1)
+    t = torch.arange(n, device="cuda")
+    cfg = lsa.LsaConfig(cli_factor=1)
+    lsa.fp8_append(cfg, (torch.from_numpy(c.table[0]).cuda()[t // 64] * 64 + t % 64).int(), [lat], c.latent_pages)
+    codes, s = F.quant(_vals(lat))
+    c.lat[0][0], c.lat_s[0][0] = F.dequant(codes, s), s
+    for ws in (None, lsa.workspace(cfg, lsa.OP_FP8_MLA, 1, 1, n)):
+        out, lse = [torch.empty(1, 32, 512, dtype=torch.bfloat16, device="cuda")], [torch.empty(1, 32, device="cuda")]
+        lsa.fp8_sparse_mla(cfg, None, _i32([n - 1]), [q], c.latent_pages, c.block_table, None, None, n, out, lse, ws)
+        assert lsa.device_error() == 0
+        want, wl, wt = F.attend(_vals(q)[0], c.lat[0][0], range(n), cfg.softmax_scale)
+        tol, ltol = _mla_tol(_vals(q)[0], c.lat[0][0], s, range(n), wt, want, cfg.softmax_scale)
+        assert (np.abs(lse[0][0].double().cpu().numpy() - wl) <= ltol).all()
+        assert (np.abs(_vals(out[0])[0] - want) <= tol).all()
+
+
+@gpu
+def test_mla_non_finite_queries_give_nan_for_their_row_alone():
+    c = Caches([200], 23, cli=1)
+    cfg = lsa.LsaConfig(cli_factor=1)
+    q = [_bf16(np.random.default_rng(0).standard_normal((3, 32, 576))).cuda()]
+    q[0][1, 5, 100] = float("inf")
+    out, lse = [torch.zeros(3, 32, 512, dtype=torch.bfloat16, device="cuda")], [torch.zeros(3, 32, device="cuda")]
+    lsa.fp8_sparse_mla(cfg, _i32([0, 0, 0]), _i32([199, 150, 60]), q, c.latent_pages, c.block_table, None, None, 200,
+                       out, lse, None)
+    assert lsa.device_error() == 0
+    assert torch.isnan(out[0][1]).all() and torch.isnan(lse[0][1]).all()
+    for r, p in ((0, 199), (2, 60)):
+        want, wl, wt = F.attend(_vals(q[0])[r], c.lat[0][0], range(p + 1), cfg.softmax_scale)
+        tol, ltol = _mla_tol(_vals(q[0])[r], c.lat[0][0], c.lat_s[0][0], range(p + 1), wt, want, cfg.softmax_scale)
+        assert (np.abs(_vals(out[0])[r] - want) <= tol).all()
+        assert (np.abs(lse[0][r].double().cpu().numpy() - wl) <= ltol).all()
 
 
 @gpu
