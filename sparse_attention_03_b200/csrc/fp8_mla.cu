@@ -18,11 +18,12 @@
 //   - the weight u = p * s_i * 2^(2 - A), at most 128, k = 64: 8 significant
 //     bits, the precision of a bf16 weight, in steps of at least 2^-15 (2^-16 of
 //     the largest u of its frame: what is below is lost).
-// The frame A of each head (an integer, so that rescaling is exact) follows the
-// running maximum of log2(p s): it is set from the first tile, raised when a u
-// would pass 128, and set anew every 16 tiles (also downwards, to 2^-60 of the
-// highest: O is then scaled up, fp32 has the range), so that the loss stays
-// relative to the 2048 keys around a key however long the list is. The sum of the
+// The frame A of each head follows the running maximum of log2(p s). It is m plus
+// an integer, m the largest logit where it was set, so that the heaviest key's u
+// is a power of two: a row of one key comes out exact. It is set from the first
+// tile, raised when a u would pass 128, and set anew every 16 tiles (also
+// downwards, to 2^-60 of the highest: O is then scaled up, fp32 has the range), so
+// that the loss stays relative to the 2048 keys around a key however long the list is. The sum of the
 // softmax is kept apart, in fp32, of the unrounded weights, in its own frame m (a
 // key's scale, which is no part of its weight, cannot disturb it).
 //
@@ -615,7 +616,7 @@ __device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& s
     float L[kHG];
 #pragma unroll
     for (int j = 0; j < kHG; ++j) L[j] = f.m[j] = f.w[j] = 0.f;
-    float m_h = 0.f, a_h = kUnset, a_top = kUnset;  // head h's frames (every warp of the group the same)
+    float m_h = 0.f, d_h = kUnset, a_h = kUnset, a_top = kUnset;  // head h's frames (the same in every warp of the group)
     bool framed = false, dead = false;
     for (int t = t0; t < t1; ++t, ++g) {
       const int b = g & 1;
@@ -663,14 +664,17 @@ __device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& s
           ta = fmaxf(ta, sm.tmax[w0 + w][h].y);
         }
         const float m_old = m_h, a_old = a_h;
-        if (tl > -INFINITY) m_h = framed ? fmaxf(m_old, ceilf(tl + m_old)) : ceilf(tl + m_old);
-        // down by at most 2^60 from the item's highest: O, scaled up by as much, stays far from overflow
-        if (ta > -INFINITY) a_h = fmaxf(ceilf(ta + m_old), anew ? a_top - 60.f : a_old);
-        a_top = fmaxf(a_top, a_h);
+        if (tl > -INFINITY) m_h = framed ? fmaxf(m_old, tl + m_old) : tl + m_old;
+        if (ta > -INFINITY) {
+          // down by at most 2^60 from the item's highest: O, scaled up by as much, stays far from overflow
+          d_h = ceilf(fmaxf(ta + m_old, anew ? a_top - 60.f : a_old) - m_h);
+          a_h = m_h + d_h;
+          a_top = fmaxf(a_top, a_h);
+        }
         framed = framed || __any_sync(0xffffffffu, tl > -INFINITY);
-        const float of = pow2f(a_old - a_h);
+        const float of = ex2(fminf(a_old - a_h, 126.f));
         __syncwarp();
-        frame[h] = make_float4(-m_h, pow2f(fminf(2.f - (a_h - m_h), 126.f)), pow2f(m_old - m_h), of);
+        frame[h] = make_float4(-m_h, pow2f(fminf(2.f - d_h, 126.f)), ex2(fminf(m_old - m_h, 126.f)), of);
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < kHG; ++j) {
@@ -728,7 +732,7 @@ __device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& s
     if (quarter == 0) {
       const float l = (sm.lsum[w0][h] + sm.lsum[w0 + 1][h]) + (sm.lsum[w0 + 2][h] + sm.lsum[w0 + 3][h]);
       const int f = nk & 3;
-      sm.fin[f][group * kHG + h] = make_float2(a_h == kUnset ? 0.f : pow2f(a_h - m_h - 2.f), l);
+      sm.fin[f][group * kHG + h] = make_float2(a_h == kUnset ? 0.f : pow2f(d_h - 2.f), l);
       sm.fin_m[f][group * kHG + h] = m_h;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.fin_full[f]);

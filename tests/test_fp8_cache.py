@@ -706,6 +706,29 @@ def test_mla_dense_with_the_weight_in_front(first):
 
 
 @gpu
+def test_mla_rows_of_one_key_are_exact():
+    # the output is the key's own value: 4 significant bits, exact in bf16 (and lse its logit)
+    c = Caches([300], 24, cli=1)
+    cfg = lsa.LsaConfig(index_topk=8, index_init_tokens=1, index_local_tokens=2, cli_factor=1)
+    keys = [0, 5, 77, 128, 299, 131]
+    n = len(keys)
+    q = [_bf16(np.random.default_rng(0).standard_normal((n, 32, 576)) * 3).cuda()]
+    idx = np.full((n, 8), -1)
+    idx[:, 0] = keys
+    out, lse = [torch.zeros(n, 32, 512, dtype=torch.bfloat16, device="cuda")], [torch.zeros(n, 32, device="cuda")]
+    lsa.fp8_sparse_mla(cfg, _i32([0] * n), _i32([299] * n), q, c.latent_pages, c.block_table, _i32(idx), _i32([1] * n), 300,
+                       out, lse, None)
+    assert lsa.device_error() == 0
+    for r, k in enumerate(keys):
+        want = np.broadcast_to(c.lat[0][0][k, :512], (32, 512))
+        np.testing.assert_array_equal(_vals(out[0])[r], want)
+        x = cfg.softmax_scale * (_vals(q[0])[r] @ c.lat[0][0][k])
+        bound = cfg.softmax_scale * (577 * 2.0 ** -23 * (np.abs(_vals(q[0])[r]) @ np.abs(c.lat[0][0][k]))
+                                     + 2.0 ** -22 * np.abs(_vals(q[0])[r]).max() * np.abs(c.lat[0][0][k]).sum()) + 2.0 ** -20
+        assert (np.abs(lse[0][r].double().cpu().numpy() - x) <= bound).all()
+
+
+@gpu
 def test_mla_non_finite_queries_give_nan_for_their_row_alone():
     c = Caches([200], 23, cli=1)
     cfg = lsa.LsaConfig(cli_factor=1)
