@@ -54,9 +54,9 @@ struct Fp8IndexArgs {
   uint32_t* hist;  // top-k histograms (zeroed by the launcher), or null
   void* ws;        // fp8_index_ws_bytes, 256-byte aligned
 };
-size_t fp8_index_ws_bytes(int n_rows, int n_seq);
+size_t fp8_index_ws_bytes(int n_rows);
 // Whether these rows take the streaming form, which builds histograms on the way.
-bool fp8_index_streams(int n_rows, int n_seq);
+bool fp8_index_streams(int n_rows, int n_seq, int64_t max_len);
 cudaError_t launch_fp8_index(const Fp8IndexArgs& a, cudaStream_t st);
 
 struct Fp8MlaArgs {

@@ -15,7 +15,7 @@ struct ForwardPlan {
   size_t topk_bytes, mla_bytes;
 };
 
-ForwardPlan forward_plan(const lsa_config* c, int R, int n_seq, int64_t max_len) {
+ForwardPlan forward_plan(const lsa_config* c, int R, int64_t max_len) {
   ForwardPlan p;
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -27,7 +27,7 @@ ForwardPlan forward_plan(const lsa_config* c, int R, int n_seq, int64_t max_len)
   p.hist = take((size_t)R * kTopkHistStride * sizeof(uint32_t));
   p.idx = take((size_t)R * c->index_topk * sizeof(int32_t));
   p.count = take((size_t)R * sizeof(int32_t));
-  p.index = take(fp8_index_ws_bytes(R, 1));  // the larger form: a block may hold rows of few sequences
+  p.index = take(fp8_index_ws_bytes(R));
   p.topk_bytes = topk_ws(R, max_len);
   p.topk = take(p.topk_bytes);
   p.mla_bytes = fp8_mla_ws_bytes(R, c->cli_factor, c->index_topk);
@@ -83,10 +83,10 @@ PagedRows paged_rows(int32_t n_rows, int32_t n_seq, const int32_t* seq_of_row, c
 }  // namespace
 
 size_t fp8_workspace_size(const lsa_config* c, int op, int n_rows, int n_seq, int64_t max_len) {
-  if (op == LSA_OP_FP8_INDEX) return fp8_index_ws_bytes(n_rows, n_seq) + kAlign;
+  if (op == LSA_OP_FP8_INDEX) return fp8_index_ws_bytes(n_rows) + kAlign;
   if (op == LSA_OP_FP8_MLA) return fp8_mla_ws_bytes(n_rows, c->cli_factor, max_len) + kAlign;
   if (max_len <= c->index_topk) return fp8_mla_ws_bytes(n_rows, c->cli_factor, max_len) + kAlign;
-  return forward_plan(c, prefill_block_rows(n_rows, max_len), n_seq, max_len).total + kAlign;
+  return forward_plan(c, prefill_block_rows(n_rows, max_len), max_len).total + kAlign;
 }
 
 }  // namespace lsa
@@ -184,7 +184,7 @@ lsa_status lsa_fp8_index_scores(const lsa_config* c, int32_t n_rows, int32_t n_s
     return set_error(LSA_ERR_INVALID, "%s: topk_hist must be 16-byte aligned", fn);
   size_t avail;
   char* base = align_ws(ws, ws_bytes, &avail);
-  const size_t need = fp8_index_ws_bytes(n_rows, n_seq);
+  const size_t need = fp8_index_ws_bytes(n_rows);
   if (avail < need) return set_error(LSA_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", fn, need + kAlign);
   Fp8IndexArgs a;
   a.rows = paged_rows(n_rows, n_seq, seq_of_row, pos, block_table, max_pages, n_pages, max_len);
@@ -261,8 +261,8 @@ lsa_status lsa_fp8_forward(const lsa_config* c, int32_t n_rows, int32_t n_seq, c
   size_t avail;
   char* base = align_ws(ws, ws_bytes, &avail);
   int R = prefill_block_rows(n_rows, max_len);
-  while (R > 1 && forward_plan(c, R, n_seq, max_len).total > avail) R = R > 64 ? R / 64 * 32 : R / 2;
-  const ForwardPlan p = forward_plan(c, R, n_seq, max_len);
+  while (R > 1 && forward_plan(c, R, max_len).total > avail) R = R > 64 ? R / 64 * 32 : R / 2;
+  const ForwardPlan p = forward_plan(c, R, max_len);
   if (p.total > avail)
     return set_error(LSA_ERR_WORKSPACE, "%s: workspace %zu below the minimum %zu", fn, ws_bytes, p.total + kAlign);
   const cudaStream_t st = (cudaStream_t)stream;
@@ -284,7 +284,7 @@ lsa_status lsa_fp8_forward(const lsa_config* c, int32_t n_rows, int32_t n_seq, c
     a.ld = max_len;
     // The streaming indexer builds the top-k's histogram from the scores in registers;
     // rows short enough that the top-k holds all their scores gain nothing from it.
-    const bool hist = fp8_index_streams(nr, rows.n_seq) &&
+    const bool hist = fp8_index_streams(nr, rows.n_seq, max_len) &&
                       max_len - c->index_init_tokens - c->index_local_tokens > kTopkShortMid;
     a.hist = hist ? reinterpret_cast<uint32_t*>(base + p.hist) : nullptr;
     a.ws = base + p.index;

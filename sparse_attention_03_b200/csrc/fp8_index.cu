@@ -12,10 +12,8 @@
 // Two kernels. A row of its own (decode) is bound by the key stream: 132 bytes a
 // key against 180 of ~730 cycles a 128-key tile for the products. Rows that
 // share their keys (a prompt's chunk) are bound by the tensor cores and the
-// ReLU-weighted sum over them: 16 rows a CTA, N = 256. The host takes the
-// second form when a sequence has four rows or more on average: there a tile
-// costs ~1100 cycles for up to 16 rows of a sequence, against ~250 (L2) to 730
-// (HBM) for each row of its own.
+// ReLU-weighted sum over them: 16 rows a CTA, N = 256. The host takes the form
+// that costs less (use_blocks).
 //
 // A tile is two pages of 64 keys, each one TMA copy of 8 KB (the 128-byte
 // swizzle) and one bulk copy of its 64 scales into a ring of their own (the
@@ -500,7 +498,7 @@ struct RunCursor {
 // sequences' tiles one after the other.
 __global__ void __launch_bounds__(kBlkThreads, 1)
     fp8_index_block_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap map_q,
-                           const __grid_constant__ Fp8IndexArgs a, const float* wq, int tiles_per_cta) {
+                           const __grid_constant__ Fp8IndexArgs a, const float* wq) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   if ((smem_u32(smem_raw) & 1023u) != 0) {
     if (threadIdx.x == 0) flag_error(a.rows.err, LSA_DEVERR_TIMEOUT);
@@ -553,8 +551,9 @@ __global__ void __launch_bounds__(kBlkThreads, 1)
   __syncthreads();
   int64_t n_all = 0;
   for (int i = 0; i < sm.n_runs; ++i) n_all += sm.run_tiles[i];
-  const int64_t t0 = (int64_t)blockIdx.y * tiles_per_cta;
-  const int n_tiles = (int)max64(0, min64(n_all - t0, blockIdx.y + 1 == gridDim.y ? n_all : (int64_t)tiles_per_cta));
+  // this CTA's share of the block's tiles (a block that straddles prompts has more)
+  const int64_t t0 = n_all * blockIdx.y / gridDim.y;
+  const int n_tiles = (int)(n_all * (blockIdx.y + 1) / gridDim.y - t0);
   if (n_tiles == 0) return;  // uniform across the CTA; nothing allocated yet
   if (warp == kMma) tmem_alloc(&sm.tmem_base, 512);
   tc_fence_before();
@@ -716,7 +715,16 @@ __global__ void __launch_bounds__(kBlkThreads, 1)
   }
 }
 
-bool use_blocks(int n_rows, int n_seq) { return n_rows >= 8 && (int64_t)n_rows >= 4 * (int64_t)n_seq; }
+// The form that these rows take, by what the two cost here (ns, measured over 1 to
+// 256 rows of 1 and 4 sequences of 2K to 128K keys): the streaming form 5 us and
+// 1.75 for each row and tile of its keys (64 rows x 128K: 117 us), the block form
+// 13 us and 9 for each tile of a block's run of rows (62 us; 8 rows x 128K: 17
+// against 19, 64 rows x 2K: 14 against 8).
+bool use_blocks(int64_t n_rows, int64_t n_seq, int64_t max_len) {
+  const int64_t tiles = (max_len + kTile - 1) / kTile;
+  const int64_t runs = (n_rows + kRows - 1) / kRows + min64(n_seq, n_rows) - 1;
+  return 4 * 8000 + 4 * 9 * runs * tiles < 7 * n_rows * tiles;
+}
 
 int sm_count() {
   static int cache[64];
@@ -795,23 +803,20 @@ cudaError_t launch_blocks(const Fp8IndexArgs& a, const CUtensorMap& map, cudaStr
   e = set_smem(fp8_index_block_kernel, (int)sizeof(BlockSmem), done);
   if (e != cudaSuccess) return e;
   // Shares of the tiles: the count whose waves of CTAs end first, a CTA's start
-  // (with its 64 KB of queries) costing about three tiles; at least 16 tiles each.
+  // (with its 64 KB of queries) costing about six tiles; at least 4 tiles each.
   const int n_blocks = (n_rows + kRows - 1) / kRows;
   const int64_t tiles = (a.rows.max_len + kTile - 1) / kTile;
   const int sms = sm_count();
-  const int64_t lo = max64(1, min64((2LL * sms + n_blocks - 1) / n_blocks, tiles / 16));
-  int64_t per = tiles, chunks = 1, best = INT64_MAX;
-  for (int64_t c = lo; c <= 4 * lo && c <= max64(1, tiles / 16); ++c) {
-    const int64_t p = (tiles + c - 1) / c, n = (tiles + p - 1) / p;
-    const int64_t cost = ((n * n_blocks + sms - 1) / sms) * (p + 3);  // waves of CTAs, each its tiles and its start
+  int64_t chunks = 1, best = INT64_MAX;
+  for (int64_t c = 1; c <= 592 && c <= max64(1, tiles / 4); ++c) {
+    const int64_t cost = ((c * n_blocks + sms - 1) / sms) * ((tiles + c - 1) / c + 6);
     if (cost < best) {
       best = cost;
-      per = p;
-      chunks = n;
+      chunks = c;
     }
   }
   e = launch_pdl(fp8_index_block_kernel, dim3((unsigned)n_blocks, (unsigned)chunks), dim3(kBlkThreads), sizeof(BlockSmem),
-                 st, map, map_q, a, (const float*)wq, (int)per);
+                 st, map, map_q, a, (const float*)wq);
   count_launches(1);
   if (e != cudaSuccess) return e;
   if (!a.hist) return cudaSuccess;
@@ -836,16 +841,15 @@ cudaError_t launch_blocks(const Fp8IndexArgs& a, const CUtensorMap& map, cudaStr
 
 }  // namespace
 
-size_t fp8_index_ws_bytes(int n_rows, int n_seq) {
-  return use_blocks(n_rows, n_seq) ? (size_t)n_rows * kHi * (kDi + sizeof(float)) : 0;
-}
+// the block form's quantised queries; asked for whichever form the rows take
+size_t fp8_index_ws_bytes(int n_rows) { return (size_t)n_rows * kHi * (kDi + sizeof(float)); }
 
-bool fp8_index_streams(int n_rows, int n_seq) { return !use_blocks(n_rows, n_seq); }
+bool fp8_index_streams(int n_rows, int n_seq, int64_t max_len) { return !use_blocks(n_rows, n_seq, max_len); }
 
 cudaError_t launch_fp8_index(const Fp8IndexArgs& a, cudaStream_t st) {
   CUtensorMap map;
   if (!page_map(&map, a.key_pages, a.rows.n_pages)) return cudaErrorInvalidValue;
-  return use_blocks(a.rows.n_rows, a.rows.n_seq) ? launch_blocks(a, map, st) : launch_rows(a, map, st);
+  return use_blocks(a.rows.n_rows, a.rows.n_seq, a.rows.max_len) ? launch_blocks(a, map, st) : launch_rows(a, map, st);
 }
 
 }  // namespace lsa

@@ -131,9 +131,8 @@ def test_index_scores_refusals():
     for i in (5, 6, 7, 14):
         assert call(**{f"_{i}": ctypes.c_void_p(0x10004)}) == lsa.LSA_ERR_INVALID, i
     assert call(_1=0, _4=None) == lsa.LSA_OK
-    n = lsa.workspace_size(lsa.LsaConfig(), lsa.OP_FP8_INDEX, 4096, 1, 16384)
-    if n > 256:  # the block form needs its quantised queries
-        assert call(_1=4096, _2=1, _15=None, _16=0) == lsa.LSA_ERR_WORKSPACE
+    assert call(_1=4096, _2=1, _15=None, _16=0) == lsa.LSA_ERR_WORKSPACE
+    assert call(_15=None, _16=0) == lsa.LSA_ERR_WORKSPACE
 
 
 def test_sparse_mla_and_forward_refusals():
@@ -516,13 +515,14 @@ def test_scores_rows_without_a_map_are_the_sequences():
 
 
 @gpu
+@pytest.mark.parametrize("bound", [None, 60000])   # the bound on the lengths decides the kernel's form
 @pytest.mark.parametrize("lens,new,pad", [([40], 40, 0), ([300], 37, 2), ([129, 700], 64, 5), ([17, 20, 260, 33], 17, 0),
                                           ([1500], 129, 1)])
-def test_scores_rows_of_prompts(lens, new, pad):
+def test_scores_rows_of_prompts(lens, new, pad, bound):
     # many rows of few sequences (blocks of rows share key tiles; a block may span sequences and end in padding)
     rows = [(s, p) for s, n in enumerate(lens) for p in range(max(0, n - new), n)] + [(-1, -1)] * pad
     for cfg in (lsa.LsaConfig(**TINY), lsa.LsaConfig(index_topk=64, index_init_tokens=0, index_local_tokens=0)):
-        err, *_ = _score_case(lens, rows, cfg, seed=len(lens), max_len=max(lens) + 11)
+        err, *_ = _score_case(lens, rows, cfg, seed=len(lens), max_len=bound or max(lens) + 11)
         assert err == 0
 
 
@@ -540,11 +540,12 @@ def _check_hist(rows, scores, h, cfg):
 
 
 @gpu
-def test_scores_of_prompt_rows_with_the_histogram():
+@pytest.mark.parametrize("bound", [None, 60000])
+def test_scores_of_prompt_rows_with_the_histogram(bound):
     lens = [300, 150]
     rows = [(s, p) for s, n in enumerate(lens) for p in range(n - 40, n)]
     cfg = lsa.LsaConfig(**TINY)
-    err, scores, pos, h, _ = _score_case(lens, rows, cfg, hist=True)
+    err, scores, pos, h, _ = _score_case(lens, rows, cfg, hist=True, max_len=bound)
     assert err == 0
     _check_hist(rows, scores, h, cfg)
 
@@ -566,11 +567,12 @@ def test_scores_of_many_short_sequences(hist):
 
 
 @gpu
-def test_scores_padding_between_rows_and_unordered_positions():
+@pytest.mark.parametrize("bound", [None, 60000])
+def test_scores_padding_between_rows_and_unordered_positions(bound):
     rng = np.random.default_rng(5)
     lens = [200, 333]
     rows = [(int(s), int(rng.integers(0, lens[s]))) if i % 5 else (-1, -1) for i, s in enumerate(rng.integers(0, 2, 70))]
-    assert _score_case(lens, rows, lsa.LsaConfig(**TINY))[0] == 0
+    assert _score_case(lens, rows, lsa.LsaConfig(**TINY), max_len=bound)[0] == 0
 
 
 @gpu
@@ -581,6 +583,7 @@ def test_scores_far_from_one(scale):
     assert _score_case(lens, [(0, 149), (1, 89)], lsa.LsaConfig(**TINY), caches=c)[0] == 0
     rows = [(0, p) for p in range(100, 150)]
     assert _score_case(lens, rows, lsa.LsaConfig(**TINY), caches=c, scale=1 / scale)[0] == 0
+    assert _score_case(lens, rows, lsa.LsaConfig(**TINY), caches=c, scale=1 / scale, max_len=60000)[0] == 0
 
 
 @gpu
@@ -595,14 +598,14 @@ def test_scores_bad_rows_and_pages(many):
     c.block_table = _i32(bad)
     base = [(0, 299), (0, 130), (1, 127), (7, 5), (-2, 3), (1, 400)]
     rows = base + ([(0, 290)] * 60 if many else [])
-    n = len(rows)
+    n, bound = len(rows), 60000 if many else 320
     rng = np.random.default_rng(0)
     q = _bf16(rng.standard_normal((n, 32, 128))).cuda()
     w = torch.from_numpy(rng.standard_normal((n, 32)).astype(np.float32)).cuda()
-    scores = torch.full((n, 320), 7.0, device="cuda")
-    ws = lsa.workspace(cfg, lsa.OP_FP8_INDEX, n, 2, 320)
+    scores = torch.full((n, bound), 7.0, device="cuda")
+    ws = lsa.workspace(cfg, lsa.OP_FP8_INDEX, n, 2, bound)
     lsa.fp8_index_scores(cfg, _i32([r[0] for r in rows]), _i32([r[1] for r in rows]), q, w, c.key_pages, c.block_table,
-                         320, scores, ws)
+                         bound, scores, ws)
     assert lsa.device_error() == lsa.DEVERR_PAGE | lsa.DEVERR_SEQ | lsa.DEVERR_POS
     got = scores.cpu().numpy()
     assert np.isneginf(got[0, 128:256]).all() and np.isfinite(got[0, 2:128]).all() and np.isinf(got[0, 296:300]).all()
@@ -621,13 +624,13 @@ def test_scores_of_non_finite_vectors_count_as_zero(many):
     c = Caches([200], 2)
     flat = c.key_pages.view(torch.float32)
     flat[int(c.table[0, 1]), 2048 + 5] = float("nan")    # key 69
-    n = 40 if many else 1
+    n, bound = (40, 60000) if many else (1, 200)
     q = _bf16(np.random.default_rng(1).standard_normal((n, 32, 128))).cuda()
     q[:, 3, 17] = float("inf")
     w = torch.ones(n, 32, device="cuda")
-    scores = torch.zeros(n, 200, device="cuda")
-    ws = lsa.workspace(cfg, lsa.OP_FP8_INDEX, n, 1, 200)
-    lsa.fp8_index_scores(cfg, _i32([0] * n), _i32([199] * n), q, w, c.key_pages, c.block_table, 200, scores, ws)
+    scores = torch.zeros(n, bound, device="cuda")
+    ws = lsa.workspace(cfg, lsa.OP_FP8_INDEX, n, 1, bound)
+    lsa.fp8_index_scores(cfg, _i32([0] * n), _i32([199] * n), q, w, c.key_pages, c.block_table, bound, scores, ws)
     assert lsa.device_error() == 0
     got = scores[:, :199].double().cpu().numpy()
     assert np.isfinite(got).all() and (got[:, 69] == 0).all()
