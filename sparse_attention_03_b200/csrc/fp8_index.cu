@@ -76,10 +76,9 @@ __device__ __forceinline__ void fma_pair(unsigned long long& s, unsigned long lo
   asm("{\n .reg .b64 x;\n mov.b64 x, {%2, %3};\n fma.rn.f32x2 %0, %1, x, %0;\n}\n" : "+l"(s) : "l"(w), "f"(x0), "f"(x1));
 }
 __device__ __forceinline__ float sum_pairs(unsigned long long a, unsigned long long b) {
-  float a0, a1, b0, b1;
-  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a0), "=f"(a1) : "l"(a));
-  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(b0), "=f"(b1) : "l"(b));
-  return (a0 + a1) + (b0 + b1);
+  float x, y;
+  asm("{\n .reg .b64 t;\n add.rn.f32x2 t, %2, %3;\n mov.b64 {%0, %1}, t;\n}\n" : "=f"(x), "=f"(y) : "l"(a), "l"(b));
+  return x + y;
 }
 
 // One row's ReLU-weighted sum over its 32 heads, w holding half the weights: the
@@ -87,17 +86,17 @@ __device__ __forceinline__ float sum_pairs(unsigned long long a, unsigned long l
 // FMAs took 188 cycles a warp with four warps a scheduler, the additions 141),
 // then two heads an instruction (packed fp32 pairs, four chains).
 __device__ __forceinline__ float weighted_sum(const uint32_t (&v)[32], const float* w) {
-  unsigned long long s[4] = {0, 0, 0, 0};
+  unsigned long long s0 = 0, s1 = 0;
   const ulonglong2* wv = reinterpret_cast<const ulonglong2*>(w);
 #pragma unroll
   for (int h4 = 0; h4 < 8; ++h4) {
     const ulonglong2 ww = wv[h4];
     const float x0 = __uint_as_float(v[4 * h4]), x1 = __uint_as_float(v[4 * h4 + 1]);
     const float x2 = __uint_as_float(v[4 * h4 + 2]), x3 = __uint_as_float(v[4 * h4 + 3]);
-    fma_pair(s[2 * (h4 & 1)], ww.x, x0 + fabsf(x0), x1 + fabsf(x1));
-    fma_pair(s[2 * (h4 & 1) + 1], ww.y, x2 + fabsf(x2), x3 + fabsf(x3));
+    fma_pair(s0, ww.x, x0 + fabsf(x0), x1 + fabsf(x1));
+    fma_pair(s1, ww.y, x2 + fabsf(x2), x3 + fabsf(x3));
   }
-  return sum_pairs(s[0], s[1]) + sum_pairs(s[2], s[3]);
+  return sum_pairs(s0, s1);
 }
 
 // Quantises one head's 128 query elements over a half warp (8 elements a lane,
@@ -164,7 +163,7 @@ __device__ __forceinline__ void drain_copies(uint64_t* full, uint64_t* sfull, ui
   const long long t0 = global_ns();
   for (uint32_t i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
     while (!mbar_try_wait(&full[i % STAGES], (i / STAGES) & 1) ||
-           !mbar_try_wait(&sfull[i % kScaleRing], (i / kScaleRing) & 1))
+           (sfull && !mbar_try_wait(&sfull[i % kScaleRing], (i / kScaleRing) & 1)))
       if (global_ns() - t0 > kWaitLimitNs) return;
 }
 
@@ -439,16 +438,17 @@ __global__ void __launch_bounds__(kDecThreads, 2)
 
 // ---------------------------------------------------------------- rows that share keys
 
-constexpr int kRows = 16;                     // rows of a CTA
+constexpr int kRows = 16;                     // rows of a block
 constexpr int kBStages = 6;
 constexpr int kEpiWarps = 16;
-static_assert(8 * 4 / kEpiWarps == 2, "rows of an accumulator that a warp sums");
+constexpr int kGroups = 2;                    // accumulators of 128 columns: 4 rows x 32 heads, four warps each
+static_assert(kRows / kEpiWarps == 1, "a warp sums four rows of a quarter of the keys");
 constexpr int kProducer = kEpiWarps, kMma = kEpiWarps + 1;  // their warps
 constexpr int kBlkThreads = (kEpiWarps + 2) * 32;
-constexpr uint32_t kBHalf = 256 * kDi;        // 8 rows x 32 heads x 128 codes: 32 KB
+constexpr uint32_t kGroupBytes = 256 * kDi;   // 4 rows x 32 heads x 128 codes: 16 KB
 
 struct __align__(1024) BlockSmem {
-  uint8_t b[2][kBHalf];
+  uint8_t b[kGroups][kGroupBytes];
   uint8_t a[kBStages][kTileBytes];
   TileScales sc[kScaleRing];
   __align__(16) float w[kRows][kHi];
@@ -456,18 +456,53 @@ struct __align__(1024) BlockSmem {
   int seq[kRows];
   // runs of rows of one sequence: its rows [run_r0, run_r1) of the block, its tiles
   int run_r0[kRows], run_r1[kRows], run_tiles[kRows], n_runs;
-  uint64_t full[kBStages], empty[kBStages], sfull[kScaleRing], tfull[2], tempty[2], qfull;
+  long long sums[kEpiWarps + 2], total;
+  int start_block, start_tile;
+  uint64_t full[kBStages], empty[kBStages], tfull[kGroups], tempty[kGroups], qfull;
   uint32_t tmem_base;
   int abort_flag;
 };
 
-// The codes and weights of all rows' queries, a half warp a head.
-__global__ void __launch_bounds__(256) fp8_index_query_kernel(const __grid_constant__ Fp8IndexArgs a, uint8_t* codes, float* wq) {
+// The tiles that a block of rows takes: the runs of rows of one sequence, each up to
+// its furthest visible key. seq[i], nvis[i]: row i's sequence (-1: none) and keys.
+template <typename F>
+__device__ __forceinline__ void block_runs(const int* seq, const int64_t* nvis, F&& run) {
+  for (int i = 0; i < kRows;) {
+    int e = i + 1;
+    int64_t most = nvis[i];
+    for (; e < kRows && seq[e] == seq[i]; ++e) most = max64(most, nvis[e]);
+    if (seq[i] >= 0 && most > 0) run(i, e, (int)((most + kTile - 1) / kTile));
+    i = e;
+  }
+}
+
+// The codes and weights of all rows' queries, a half warp a head, and every block's
+// tiles (a CTA has the 16 heads of half a row: every 32nd takes a block).
+__global__ void __launch_bounds__(256) fp8_index_query_kernel(const __grid_constant__ Fp8IndexArgs a, uint8_t* codes,
+                                                              float* wq, int* block_tiles) {
   pdl_wait();
   const int64_t head = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 4;
   const int sub = threadIdx.x & 15;
   const bool live = head < (int64_t)a.rows.n_rows * kHi;
   const uint4 v = live ? __ldg(reinterpret_cast<const uint4*>(a.q_idx + head * kDi) + sub) : make_uint4(0, 0, 0, 0);
+  if (blockIdx.x % (2 * kRows) == 0 && threadIdx.x < 32) {
+    __shared__ int seq[kRows];
+    __shared__ int64_t nvis[kRows];
+    const int block = blockIdx.x / (2 * kRows), r = block * kRows + threadIdx.x;
+    if (threadIdx.x < kRows) {
+      PagedGeom g = {-1, true, 0};
+      if (r < a.rows.n_rows) g = paged_geom(a.rows, r, true);
+      seq[threadIdx.x] = g.seq;
+      nvis[threadIdx.x] = g.nvis;
+    }
+    __syncwarp();
+    if (threadIdx.x == 0) {
+      int n = 0;
+      block_runs(seq, nvis, [&](int, int, int tiles) { n += tiles; });
+      block_tiles[block] = n;
+    }
+    __syncwarp();
+  }
   float scale;
   const uint2 c = quant_head(v, scale);
   if (!live) return;
@@ -492,13 +527,15 @@ struct RunCursor {
   }
 };
 
-// One CTA: 16 consecutive rows against a share of their key tiles. Warps: sixteen
-// for the epilogue (2 rows x 32 heads of an accumulator each; a thread = a key), TMA
-// producer, MMA (tile x 8 rows x 32 heads twice, two 256-column accumulators). Rows of several sequences (a block that straddles prompts) take their
-// sequences' tiles one after the other.
+// Persistent: the tiles of all blocks of 16 rows (the furthest rows' block first)
+// make one list, of which every CTA takes an equal share, block after block. Warps:
+// sixteen for the epilogue, TMA producer, MMA. A tile's products are four
+// accumulators of 4 rows x 32 heads, each with its own four epilogue warps (a thread
+// = a key), so a group's sums wait for nobody else's. Rows of several sequences (a
+// block that straddles prompts) take their sequences' tiles one after the other.
 __global__ void __launch_bounds__(kBlkThreads, 1)
     fp8_index_block_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap map_q,
-                           const __grid_constant__ Fp8IndexArgs a, const float* wq) {
+                           const __grid_constant__ Fp8IndexArgs a, const float* wq, const int* block_tiles) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   if ((smem_u32(smem_raw) & 1023u) != 0) {
     if (threadIdx.x == 0) flag_error(a.rows.err, LSA_DEVERR_TIMEOUT);
@@ -506,206 +543,227 @@ __global__ void __launch_bounds__(kBlkThreads, 1)
   }
   BlockSmem& sm = *reinterpret_cast<BlockSmem*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_wait();
-  // the latest blocks (of a causal chunk: the longest) first
-  const int row0 = (gridDim.x - 1 - blockIdx.x) * kRows;
-  if (tid < kRows) {
-    const int r = row0 + tid;
-    PagedGeom g = {-1, true, 0};
-    if (r < a.rows.n_rows) g = paged_geom(a.rows, r, blockIdx.y == 0);
-    sm.seq[tid] = g.seq;
-    sm.nvis[tid] = g.nvis;
-  }
-  for (int i = tid; i < kRows * kHi; i += kBlkThreads)
-    sm.w[i / kHi][i % kHi] = row0 + i / kHi < a.rows.n_rows ? 0.5f * wq[(int64_t)row0 * kHi + i] : 0.f;
+  const int n_blocks = (a.rows.n_rows + kRows - 1) / kRows;
   if (tid == 0) {
     for (int s = 0; s < kBStages; ++s) {
-      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.full[s], 2);  // load_tile's two announcements
       mbar_init(&sm.empty[s], 1);
     }
-    for (int i = 0; i < kScaleRing; ++i) mbar_init(&sm.sfull[i], 1);
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&sm.tfull[b], 1);
-      mbar_init(&sm.tempty[b], kEpiWarps);
+    for (int b = 0; b < kGroups; ++b) {
+      mbar_init(&sm.tfull[b], 2);  // the products' commit, and the MMA warp's own arrival
+      mbar_init(&sm.tempty[b], kEpiWarps / kGroups);
     }
     mbar_init(&sm.qfull, 1);
     sm.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::);
   }
-  __syncthreads();
-  if (tid == 0) {
-    int n = 0;
-    for (int i = 0; i < kRows;) {
-      int e = i + 1;
-      int64_t most = sm.nvis[i];
-      for (; e < kRows && sm.seq[e] == sm.seq[i]; ++e) most = max64(most, sm.nvis[e]);
-      if (sm.seq[i] >= 0 && most > 0) {
-        sm.run_r0[n] = i;
-        sm.run_r1[n] = e;
-        sm.run_tiles[n++] = (int)((most + kTile - 1) / kTile);
-      }
-      i = e;
-    }
-    sm.n_runs = n;
-  }
-  __syncthreads();
-  int64_t n_all = 0;
-  for (int i = 0; i < sm.n_runs; ++i) n_all += sm.run_tiles[i];
-  // this CTA's share of the block's tiles (a block that straddles prompts has more)
-  const int64_t t0 = n_all * blockIdx.y / gridDim.y;
-  const int n_tiles = (int)(n_all * (blockIdx.y + 1) / gridDim.y - t0);
-  if (n_tiles == 0) return;  // uniform across the CTA; nothing allocated yet
   if (warp == kMma) tmem_alloc(&sm.tmem_base, 512);
+  pdl_wait();
+  // This CTA's share [lo, hi) of the list: block n_blocks - 1 first. A thread sums
+  // `per` consecutive blocks, a warp its threads, and the thread in whose part lo
+  // lies walks it.
+  const int per = (n_blocks + kBlkThreads - 1) / kBlkThreads;
+  const int b0 = min(tid * per, n_blocks), b1 = min(b0 + per, n_blocks);  // places in the list
+  long long part = 0;
+  for (int b = b0; b < b1; ++b) part += block_tiles[n_blocks - 1 - b];
+  long long before = part;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, before, off);
+    if (lane >= off) before += o;
+  }
+  if (lane == 31) sm.sums[warp] = before;
+  before -= part;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  long long total = 0;
+  for (int i = 0; i < kEpiWarps + 2; ++i) {
+    if (i == warp) before += total;
+    total += sm.sums[i];
+  }
+  const long long lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
+  if (lo < hi && before <= lo && lo < before + part) {
+    int b = b0;
+    for (long long at = before;; ++b) {
+      const int n = block_tiles[n_blocks - 1 - b];
+      if (lo < at + n) {
+        sm.start_tile = (int)(lo - at);
+        break;
+      }
+      at += n;
+    }
+    sm.start_block = n_blocks - 1 - b;
+  }
+  __syncthreads();
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort_flag = &sm.abort_flag;
+  int block = sm.start_block, first_tile = sm.start_tile;
+  long long left = hi - lo;
+  uint32_t g = 0;  // tiles of the CTA before this block's
 
-  RunCursor cur;
-  cur.start(sm, (int)t0);
-  if (warp == kProducer) {
-    // ---------------- producer ----------------
-    if (lane == 0) {
-      mbar_expect_tx(&sm.qfull, 2 * kBHalf);
-      for (int q = 0; q < 2; ++q) tma_load_2d(sm.b[q], &map_q, 0, row0 * kHi + q * 256, &sm.qfull);
+  for (uint32_t seg = 0; left > 0; --block, first_tile = 0) {
+    const int n_tiles = (int)min64(block_tiles[block] - first_tile, left);
+    if (n_tiles == 0) continue;  // padding
+    const int row0 = block * kRows;
+    if (tid < kRows) {
+      PagedGeom geom = {-1, true, 0};
+      if (row0 + tid < a.rows.n_rows) geom = paged_geom(a.rows, row0 + tid, false);
+      sm.seq[tid] = geom.seq;
+      sm.nvis[tid] = geom.nvis;
     }
-    __syncwarp();
-    int pages = 0, batch_run = -1, batch = 0, i = 0;
-    int64_t most = 0;
-    for (; i < n_tiles; ++i, cur.next(sm)) {
-      if (cur.run != batch_run || cur.tile - batch >= 16) {
-        if (cur.run != batch_run) {
-          most = 0;
-          for (int r = sm.run_r0[cur.run]; r < sm.run_r1[cur.run]; ++r) most = max64(most, sm.nvis[r]);
-        }
-        batch_run = cur.run;
-        batch = cur.tile;
-        pages = lookup_pages(a.rows, sm.seq[sm.run_r0[cur.run]], most, 2 * (int64_t)batch, lane);
-      }
-      const int in_batch = cur.tile - batch;
-      const int p0 = __shfl_sync(0xffffffffu, pages, 2 * in_batch), p1 = __shfl_sync(0xffffffffu, pages, 2 * in_batch + 1);
-      const int s = i % kBStages;
-      if (i >= kBStages && !mbar_wait_fast(&sm.empty[s], ((i / kBStages) - 1) & 1, abort_flag)) break;
+    for (int i = tid; i < kRows * kHi; i += kBlkThreads)
+      sm.w[i / kHi][i % kHi] = row0 + i / kHi < a.rows.n_rows ? 0.5f * wq[(int64_t)row0 * kHi + i] : 0.f;
+    if (warp == 0) {
       __syncwarp();
-      if (lane == 0)
-        load_tile(&map, a.key_pages, p0, p1, sm.a[s], &sm.sc[i % kScaleRing], &sm.full[s], &sm.sfull[i % kScaleRing]);
-      __syncwarp();
-    }
-    if (*abort_flag) {
-      drain_copies<kBStages>(sm.full, sm.sfull, i);
-      const long long t_out = global_ns();
-      while (!mbar_try_wait(&sm.qfull, 0) && global_ns() - t_out < kWaitLimitNs) {
+      if (lane == 0) {
+        int n = 0;
+        block_runs(sm.seq, sm.nvis, [&](int r0, int r1, int tiles) {
+          sm.run_r0[n] = r0;
+          sm.run_r1[n] = r1;
+          sm.run_tiles[n++] = tiles;
+        });
+        sm.n_runs = n;
       }
     }
-  } else if (warp == kMma) {
-    // ---------------- MMA ----------------
-    const uint32_t leader = elect_one();
-    bool ok = mbar_wait_fast(&sm.qfull, 0, abort_flag);
-    const uint32_t b_addr = smem_u32(sm.b[0]);
-    for (int i = 0; ok && i < n_tiles; ++i) {
-      const int s = i % kBStages;
-      if (!mbar_wait_fast(&sm.full[s], (i / kBStages) & 1, abort_flag)) break;
-      const uint64_t ad = sw128_desc(smem_u32(sm.a[s]));
-      for (int hb = 0; hb < 2; ++hb) {
-        if (i > 0 && !mbar_wait_fast(&sm.tempty[hb], (i - 1) & 1, abort_flag)) {
-          ok = false;
-          break;
-        }
-        __syncwarp();
-        tc_fence_after();
-        const uint64_t bd = sw128_desc(b_addr + hb * kBHalf);
-#pragma unroll
-        for (int c = 0; c < kDi / 32; ++c)
-          umma_f8(tmem + hb * 256, ad + (c * 32 >> 4), bd + (c * 32 >> 4), f8_idesc(256, false), c > 0 ? 1u : 0u, leader);
-        if (leader) {
-          umma_commit(&sm.tfull[hb]);
-          if (hb == 1) umma_commit(&sm.empty[s]);
-        }
-        __syncwarp();
-      }
+    if (warp == kProducer && lane == 0) {  // the last block's products have been read: the queries' place is free
+      mbar_expect_tx(&sm.qfull, kGroups * kGroupBytes);
+      for (int q = 0; q < kGroups; ++q) tma_load_2d(sm.b[q], &map_q, 0, row0 * kHi + q * 256, &sm.qfull);
     }
-  } else if (warp < kEpiWarps) {
-    // ---------------- epilogue ----------------
-    const int quarter = warp & 3, part = warp >> 2;
-    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    const int lane_j = quarter * 32 + lane;
-    // This warp's rows: 2 part and 2 part + 1 of each accumulator.
-    float* out[4];
-    int32_t nvis[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int row = (u >> 1) * 8 + part * 2 + (u & 1);
-      out[u] = a.scores + (int64_t)(row0 + row) * a.ld + lane_j;
-      nvis[u] = (int32_t)min64(sm.nvis[row], INT32_MAX);
-    }
-    int run = -1, tiles_left = 0, mine = 0, lo_key = 0, hi_key = 0;
-    for (int i = 0; i < n_tiles; ++i) {
-      if (tiles_left == 0) {  // a run begins: which of the warp's rows are in it, and the keys that no row treats apart
-        run = cur.run;
-        const int r0 = sm.run_r0[run], r1 = sm.run_r1[run];
-        tiles_left = sm.run_tiles[run] - cur.tile;
-        mine = 0;
-        lo_key = a.n_init;
-        hi_key = INT32_MAX;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int row = (u >> 1) * 8 + part * 2 + (u & 1);
-          if (row >= r0 && row < r1) {
-            mine |= 1 << u;
-            hi_key = min(hi_key, max(nvis[u] - a.n_loc, 0));
+    __syncthreads();
+    RunCursor cur;
+    cur.start(sm, first_tile);
+    if (warp == kProducer) {
+      // ---------------- producer ----------------
+      int pages = 0, batch_run = -1, batch = 0;
+      int64_t most = 0;
+      uint32_t i = g;
+      for (; i < g + n_tiles; ++i, cur.next(sm)) {
+        if (cur.run != batch_run || cur.tile - batch >= 16) {
+          if (cur.run != batch_run) {
+            most = 0;
+            for (int r = sm.run_r0[cur.run]; r < sm.run_r1[cur.run]; ++r) most = max64(most, sm.nvis[r]);
           }
+          batch_run = cur.run;
+          batch = cur.tile;
+          pages = lookup_pages(a.rows, sm.seq[sm.run_r0[cur.run]], most, 2 * (int64_t)batch, lane);
+        }
+        const int in_batch = cur.tile - batch;
+        const int p0 = __shfl_sync(0xffffffffu, pages, 2 * in_batch), p1 = __shfl_sync(0xffffffffu, pages, 2 * in_batch + 1);
+        const int s = i % kBStages;
+        if (i >= kBStages && !mbar_wait_fast(&sm.empty[s], ((i / kBStages) - 1) & 1, abort_flag)) break;
+        __syncwarp();
+        if (lane == 0)
+          load_tile(&map, a.key_pages, p0, p1, sm.a[s], &sm.sc[i % kScaleRing], &sm.full[s], &sm.full[s]);
+        __syncwarp();
+      }
+      if (*abort_flag) {
+        drain_copies<kBStages>(sm.full, nullptr, i);
+        const long long t_out = global_ns();
+        while (!mbar_try_wait(&sm.qfull, seg & 1) && global_ns() - t_out < kWaitLimitNs) {
         }
       }
-      const int sr = i % kScaleRing;
-      if (!mbar_wait_fast(&sm.sfull[sr], (i / kScaleRing) & 1, abort_flag)) break;
-      const bool there = sm.sc[sr].ok[quarter >> 1] != 0;
-      const float sk = score_value(1.f, sm.sc[sr].s[lane_j]);
-      const int first = cur.tile * kTile;
-      // Most tiles: every key is there, visible to every row of the warp and forced for none.
-      const bool plain = there && mine == 15 && first >= lo_key && first <= hi_key - kTile;
-      bool ok = true;
+    } else if (warp == kMma) {
+      // ---------------- MMA ----------------
+      const uint32_t leader = elect_one();
+      bool ok = mbar_wait_fast(&sm.qfull, seg & 1, abort_flag);
+      for (uint32_t i = g; ok && i < g + n_tiles; ++i) {
+        const int s = i % kBStages;
+        if (!mbar_wait_fast(&sm.full[s], (i / kBStages) & 1, abort_flag)) break;
+        const uint64_t ad = sw128_desc(smem_u32(sm.a[s]));
+        for (int q = 0; q < kGroups; ++q) {
+          if (i > 0 && !mbar_wait_fast(&sm.tempty[q], (i - 1) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          __syncwarp();
+          tc_fence_after();
+          const uint64_t bd = sw128_desc(smem_u32(sm.b[q]));
 #pragma unroll
-      for (int hb = 0; hb < 2; ++hb) {
-        if (!mbar_wait_fast(&sm.tfull[hb], i & 1, abort_flag)) {
-          ok = false;
-          break;
+          for (int c = 0; c < kDi / 32; ++c)
+            umma_f8(tmem + q * 256, ad + (c * 32 >> 4), bd + (c * 32 >> 4), f8_idesc(256, false), c > 0 ? 1u : 0u, leader);
+          if (leader) {
+            umma_commit(&sm.tfull[q]);
+            mbar_arrive(&sm.tfull[q]);
+            if (q == kGroups - 1) umma_commit(&sm.empty[s]);
+          }
+          __syncwarp();
         }
+      }
+    } else {
+      // ---------------- epilogue ----------------
+      const int quarter = warp & 3, group = warp >> 3, row_in = (warp >> 2) * 4;  // its four rows
+      const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + row_in * 32;
+      const int lane_j = quarter * 32 + lane;
+      const float(*wrow)[kHi] = sm.w + row_in;
+      float* o = a.scores + (int64_t)(row0 + row_in) * a.ld + (int64_t)cur.tile * kTile + lane_j;
+      // Of a run: its tiles to come, the warp's rows in it, and the tiles [plain_lo,
+      // plain_hi) whose keys are visible to all of the four and forced for none.
+      int tiles_left = 0, mine = 0, plain_lo = 0, plain_hi = 0;
+      for (uint32_t i = g; i < g + n_tiles; ++i) {
+        if (tiles_left == 0) {
+          const int r0 = sm.run_r0[cur.run], r1 = sm.run_r1[cur.run];
+          tiles_left = sm.run_tiles[cur.run] - cur.tile;
+          mine = 0;
+          int64_t most = INT64_MAX;
+          for (int u = 0; u < 4; ++u) {
+            if (row_in + u >= r0 && row_in + u < r1) {
+              mine |= 1 << u;
+              most = min64(most, sm.nvis[row_in + u] - a.n_loc);
+            }
+          }
+          plain_lo = (a.n_init + kTile - 1) / kTile;
+          plain_hi = mine == 15 ? (int)(max64(most, 0) / kTile) : 0;
+        }
+        // What the MMA warp saw (the tile's scales in place) holds here too: it arrives on tfull as its commit does.
+        if (!mbar_wait_fast(&sm.tfull[group], i & 1, abort_flag)) break;
         __syncwarp();
         tc_fence_after();
-        // Two rows of this accumulator; it goes back to the MMA warp before the sums.
-        const uint32_t at = tmem + lanes + hb * 256 + part * 64;
-        uint32_t v[2][32];
-        tmem_ld32_request(at, v[0]);
-        tmem_ld32_request(at + 32, v[1]);
-        tmem_ld32_wait(v[0]);
-        tmem_ld32_wait(v[1]);
+        // Two rows at a time; the accumulator goes back before the last two are summed.
+        uint32_t v0[32], v1[32];
+        tmem_ld32_request(at, v0);
+        tmem_ld32_request(at + 32, v1);
+        const TileScales& sc = sm.sc[i % kScaleRing];
+        const bool there = sc.ok[quarter >> 1] != 0;
+        const float sk = score_value(1.f, sc.s[lane_j]);
+        const bool plain = there && cur.tile >= plain_lo && cur.tile < plain_hi;
+        auto put = [&](int u, float x) {
+          if (plain) {
+            o[u * a.ld] = x;
+          } else if (mine >> u & 1) {
+            const int64_t j = (int64_t)cur.tile * kTile + lane_j, n = sm.nvis[row_in + u];
+            if (j < n) o[u * a.ld] = j < a.n_init || j >= n - a.n_loc ? INFINITY : there ? x : -INFINITY;
+          }
+        };
+        tmem_ld32_wait(v0);
+        tmem_ld32_wait(v1);
+        put(0, weighted_sum(v0, wrow[0]) * sk);
+        tmem_ld32_request(at + 64, v0);
+        put(1, weighted_sum(v1, wrow[1]) * sk);
+        tmem_ld32_request(at + 96, v1);
+        tmem_ld32_wait(v0);
+        tmem_ld32_wait(v1);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.tempty[hb]);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int u = 2 * hb + k;
-          if (!(mine >> u & 1)) continue;
-          const float x = weighted_sum(v[k], sm.w[hb * 8 + part * 2 + k]) * sk;
-          if (plain) {
-            out[u][first] = x;
-          } else {
-            const int j = first + lane_j;
-            if (j < nvis[u])
-              out[u][first] = j < a.n_init || j >= nvis[u] - a.n_loc ? INFINITY : there ? x : -INFINITY;
-          }
+        if (lane == 0) mbar_arrive(&sm.tempty[group]);
+        put(2, weighted_sum(v0, wrow[2]) * sk);
+        put(3, weighted_sum(v1, wrow[3]) * sk);
+        ++cur.tile;
+        o += kTile;
+        if (--tiles_left == 0) {
+          --cur.tile;
+          cur.next(sm);
+          o = a.scores + (int64_t)(row0 + row_in) * a.ld + lane_j;
         }
       }
-      if (!ok) break;
-      ++cur.tile;
-      if (--tiles_left == 0) {
-        --cur.tile;
-        cur.next(sm);
-      }
     }
+    __syncwarp();
+    __syncthreads();
+    if (*abort_flag) break;
+    ++seg;
+    g += n_tiles;
+    left -= n_tiles;
   }
-  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && sm.abort_flag) flag_error(a.rows.err, LSA_DEVERR_TIMEOUT);
@@ -759,7 +817,7 @@ bool page_map(CUtensorMap* m, const void* base, int n_pages) {
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// Query codes: n rows of 128, a box is 256 of them.
+// Query codes: n rows of 128, a box is 128 of them.
 bool query_map(CUtensorMap* m, const void* base, int64_t n) {
   const auto fn = tensor_map_encode();
   if (!fn) return false;
@@ -794,29 +852,20 @@ cudaError_t launch_blocks(const Fp8IndexArgs& a, const CUtensorMap& map, cudaStr
   const int n_rows = a.rows.n_rows;
   uint8_t* codes = static_cast<uint8_t*>(a.ws);
   float* wq = reinterpret_cast<float*>(codes + (size_t)n_rows * kHi * kDi);
+  int* block_tiles = reinterpret_cast<int*>(wq + (size_t)n_rows * kHi);
   CUtensorMap map_q;
   if (!query_map(&map_q, codes, (int64_t)n_rows * kHi)) return cudaErrorInvalidValue;
   cudaError_t e = launch_pdl(fp8_index_query_kernel, dim3((unsigned)(((int64_t)n_rows * kHi * 16 + 255) / 256)), dim3(256), 0,
-                             st, a, codes, wq);
+                             st, a, codes, wq, block_tiles);
   count_launches(1);
   if (e != cudaSuccess) return e;
   e = set_smem(fp8_index_block_kernel, (int)sizeof(BlockSmem), done);
   if (e != cudaSuccess) return e;
-  // Shares of the tiles: the count whose waves of CTAs end first, a CTA's start
-  // (with its 64 KB of queries) costing about six tiles; at least 4 tiles each.
-  const int n_blocks = (n_rows + kRows - 1) / kRows;
-  const int64_t tiles = (a.rows.max_len + kTile - 1) / kTile;
-  const int sms = sm_count();
-  int64_t chunks = 1, best = INT64_MAX;
-  for (int64_t c = 1; c <= 592 && c <= max64(1, tiles / 4); ++c) {
-    const int64_t cost = ((c * n_blocks + sms - 1) / sms) * ((tiles + c - 1) / c + 6);
-    if (cost < best) {
-      best = cost;
-      chunks = c;
-    }
-  }
-  e = launch_pdl(fp8_index_block_kernel, dim3((unsigned)n_blocks, (unsigned)chunks), dim3(kBlkThreads), sizeof(BlockSmem),
-                 st, map, map_q, a, (const float*)wq);
+  // A CTA's start costs about four tiles: a share is no smaller.
+  const int64_t tiles = (n_rows + kRows - 1) / kRows * ((a.rows.max_len + kTile - 1) / kTile);
+  const unsigned ctas = (unsigned)max64(1, min64(sm_count(), tiles / 4));
+  e = launch_pdl(fp8_index_block_kernel, dim3(ctas), dim3(kBlkThreads), sizeof(BlockSmem), st, map, map_q, a,
+                 (const float*)wq, (const int*)block_tiles);
   count_launches(1);
   if (e != cudaSuccess) return e;
   if (!a.hist) return cudaSuccess;
@@ -841,8 +890,10 @@ cudaError_t launch_blocks(const Fp8IndexArgs& a, const CUtensorMap& map, cudaStr
 
 }  // namespace
 
-// the block form's quantised queries; asked for whichever form the rows take
-size_t fp8_index_ws_bytes(int n_rows) { return (size_t)n_rows * kHi * (kDi + sizeof(float)); }
+// the block form's quantised queries and tile counts; asked for whichever form the rows take
+size_t fp8_index_ws_bytes(int n_rows) {
+  return (size_t)n_rows * kHi * (kDi + sizeof(float)) + (size_t)((n_rows + kRows - 1) / kRows) * sizeof(int);
+}
 
 bool fp8_index_streams(int n_rows, int n_seq, int64_t max_len) { return !use_blocks(n_rows, n_seq, max_len); }
 
