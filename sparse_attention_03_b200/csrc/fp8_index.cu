@@ -81,20 +81,21 @@ __device__ __forceinline__ float sum_pairs(unsigned long long a, unsigned long l
   return x + y;
 }
 
-// One row's ReLU-weighted sum over its 32 heads, w holding half the weights: the
-// ReLU as x + |x| = 2 max(x, 0), one addition at full rate (32 maxima and their
-// FMAs took 188 cycles a warp with four warps a scheduler, the additions 141),
-// then two heads an instruction (packed fp32 pairs, four chains).
-__device__ __forceinline__ float weighted_sum(const uint32_t (&v)[32], const float* w) {
-  unsigned long long s0 = 0, s1 = 0;
-  const ulonglong2* wv = reinterpret_cast<const ulonglong2*>(w);
+// One row's 32 weights for ReLU-weighted sums: volatile, so that they are asked for
+// where this stands, while a tcgen05.ld is under way.
+__device__ __forceinline__ void load_weights(ulonglong2 (&w)[8], const float* row) {
+  const uint32_t p = smem_u32(row);
 #pragma unroll
-  for (int h4 = 0; h4 < 8; ++h4) {
-    const ulonglong2 ww = wv[h4];
-    const float x0 = __uint_as_float(v[4 * h4]), x1 = __uint_as_float(v[4 * h4 + 1]);
-    const float x2 = __uint_as_float(v[4 * h4 + 2]), x3 = __uint_as_float(v[4 * h4 + 3]);
-    fma_pair(s0, ww.x, x0 + fabsf(x0), x1 + fabsf(x1));
-    fma_pair(s1, ww.y, x2 + fabsf(x2), x3 + fabsf(x3));
+  for (int i = 0; i < 8; ++i) asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];\n" : "=l"(w[i].x), "=l"(w[i].y) : "r"(p + i * 16));
+}
+
+// The row's sum of w max(0, x), two heads an instruction (packed fp32 pairs).
+__device__ __forceinline__ float weighted_sum(const uint32_t (&v)[32], const ulonglong2 (&w)[8]) {
+  unsigned long long s0 = 0, s1 = 0;
+#pragma unroll
+  for (int h = 0; h < 32; h += 4) {
+    fma_pair(s0, w[h / 4].x, fmaxf(__uint_as_float(v[h]), 0.f), fmaxf(__uint_as_float(v[h + 1]), 0.f));
+    fma_pair(s1, w[h / 4].y, fmaxf(__uint_as_float(v[h + 2]), 0.f), fmaxf(__uint_as_float(v[h + 3]), 0.f));
   }
   return sum_pairs(s0, s1);
 }
@@ -441,11 +442,11 @@ __global__ void __launch_bounds__(kDecThreads, 2)
 constexpr int kRows = 16;                     // rows of a block
 constexpr int kBStages = 6;
 constexpr int kEpiWarps = 16;
-constexpr int kGroups = 2;                    // accumulators of 128 columns: 4 rows x 32 heads, four warps each
+constexpr int kGroups = 4;                    // accumulators of 128 columns: 4 rows x 32 heads, four warps each
 static_assert(kRows / kEpiWarps == 1, "a warp sums four rows of a quarter of the keys");
 constexpr int kProducer = kEpiWarps, kMma = kEpiWarps + 1;  // their warps
 constexpr int kBlkThreads = (kEpiWarps + 2) * 32;
-constexpr uint32_t kGroupBytes = 256 * kDi;   // 4 rows x 32 heads x 128 codes: 16 KB
+constexpr uint32_t kGroupBytes = 128 * kDi;   // 4 rows x 32 heads x 128 codes: 16 KB
 
 struct __align__(1024) BlockSmem {
   uint8_t b[kGroups][kGroupBytes];
@@ -533,6 +534,14 @@ struct RunCursor {
 // accumulators of 4 rows x 32 heads, each with its own four epilogue warps (a thread
 // = a key), so a group's sums wait for nobody else's. Rows of several sequences (a
 // block that straddles prompts) take their sequences' tiles one after the other.
+//
+// 4096 rows x 16K keys: 269 us, 1.79 PFLOP/s. The products alone (no sums, no
+// stores) run in 180; the sums (a maximum a product, an FMA for two, eight loads of
+// weights a row and key quarter: ~70 instructions, 16 rows a scheduler and tile)
+// need 1150 cycles a tile beside the products' 1030 and get 62% of the issue slots.
+// Measured and not kept: two accumulators of 256 columns (301), eight epilogue warps
+// with three rows in flight (365), half rows with the next half's load in flight
+// (269), x + |x| for max(0, x) (272).
 __global__ void __launch_bounds__(kBlkThreads, 1)
     fp8_index_block_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap map_q,
                            const __grid_constant__ Fp8IndexArgs a, const float* wq, const int* block_tiles) {
@@ -613,7 +622,7 @@ __global__ void __launch_bounds__(kBlkThreads, 1)
       sm.nvis[tid] = geom.nvis;
     }
     for (int i = tid; i < kRows * kHi; i += kBlkThreads)
-      sm.w[i / kHi][i % kHi] = row0 + i / kHi < a.rows.n_rows ? 0.5f * wq[(int64_t)row0 * kHi + i] : 0.f;
+      sm.w[i / kHi][i % kHi] = row0 + i / kHi < a.rows.n_rows ? wq[(int64_t)row0 * kHi + i] : 0.f;
     if (warp == 0) {
       __syncwarp();
       if (lane == 0) {
@@ -628,7 +637,7 @@ __global__ void __launch_bounds__(kBlkThreads, 1)
     }
     if (warp == kProducer && lane == 0) {  // the last block's products have been read: the queries' place is free
       mbar_expect_tx(&sm.qfull, kGroups * kGroupBytes);
-      for (int q = 0; q < kGroups; ++q) tma_load_2d(sm.b[q], &map_q, 0, row0 * kHi + q * 256, &sm.qfull);
+      for (int q = 0; q < kGroups; ++q) tma_load_2d(sm.b[q], &map_q, 0, row0 * kHi + q * 128, &sm.qfull);
     }
     __syncthreads();
     RunCursor cur;
@@ -681,7 +690,7 @@ __global__ void __launch_bounds__(kBlkThreads, 1)
           const uint64_t bd = sw128_desc(smem_u32(sm.b[q]));
 #pragma unroll
           for (int c = 0; c < kDi / 32; ++c)
-            umma_f8(tmem + q * 256, ad + (c * 32 >> 4), bd + (c * 32 >> 4), f8_idesc(256, false), c > 0 ? 1u : 0u, leader);
+            umma_f8(tmem + q * 128, ad + (c * 32 >> 4), bd + (c * 32 >> 4), f8_idesc(128, false), c > 0 ? 1u : 0u, leader);
           if (leader) {
             umma_commit(&sm.tfull[q]);
             mbar_arrive(&sm.tfull[q]);
@@ -692,7 +701,7 @@ __global__ void __launch_bounds__(kBlkThreads, 1)
       }
     } else {
       // ---------------- epilogue ----------------
-      const int quarter = warp & 3, group = warp >> 3, row_in = (warp >> 2) * 4;  // its four rows
+      const int quarter = warp & 3, group = warp >> 2, row_in = (warp >> 2) * 4;  // its four rows
       const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + row_in * 32;
       const int lane_j = quarter * 32 + lane;
       const float(*wrow)[kHi] = sm.w + row_in;
@@ -719,10 +728,11 @@ __global__ void __launch_bounds__(kBlkThreads, 1)
         if (!mbar_wait_fast(&sm.tfull[group], i & 1, abort_flag)) break;
         __syncwarp();
         tc_fence_after();
-        // Two rows at a time; the accumulator goes back before the last two are summed.
-        uint32_t v0[32], v1[32];
-        tmem_ld32_request(at, v0);
-        tmem_ld32_request(at + 32, v1);
+        // A row at a time, its weights on the way with its products.
+        uint32_t v[32];
+        ulonglong2 w[8];
+        tmem_ld32_request(at, v);
+        load_weights(w, wrow[0]);
         const TileScales& sc = sm.sc[i % kScaleRing];
         const bool there = sc.ok[quarter >> 1] != 0;
         const float sk = score_value(1.f, sc.s[lane_j]);
@@ -735,19 +745,21 @@ __global__ void __launch_bounds__(kBlkThreads, 1)
             if (j < n) o[u * a.ld] = j < a.n_init || j >= n - a.n_loc ? INFINITY : there ? x : -INFINITY;
           }
         };
-        tmem_ld32_wait(v0);
-        tmem_ld32_wait(v1);
-        put(0, weighted_sum(v0, wrow[0]) * sk);
-        tmem_ld32_request(at + 64, v0);
-        put(1, weighted_sum(v1, wrow[1]) * sk);
-        tmem_ld32_request(at + 96, v1);
-        tmem_ld32_wait(v0);
-        tmem_ld32_wait(v1);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.tempty[group]);
-        put(2, weighted_sum(v0, wrow[2]) * sk);
-        put(3, weighted_sum(v1, wrow[3]) * sk);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          tmem_ld32_wait(v);
+          if (u == 3) {  // the accumulator's last row is in registers
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.tempty[group]);
+          }
+          const float x = weighted_sum(v, w) * sk;
+          if (u < 3) {
+            tmem_ld32_request(at + (u + 1) * 32, v);
+            load_weights(w, wrow[u + 1]);
+          }
+          put(u, x);
+        }
         ++cur.tile;
         o += kTile;
         if (--tiles_left == 0) {
@@ -773,15 +785,17 @@ __global__ void __launch_bounds__(kBlkThreads, 1)
   }
 }
 
+// The most runs of rows of one sequence that the blocks can have.
+int64_t most_runs(int64_t n_rows, int64_t n_seq) { return (n_rows + kRows - 1) / kRows + min64(n_seq, n_rows) - 1; }
+
 // The form that these rows take, by what the two cost here (ns, measured over 1 to
-// 256 rows of 1 and 4 sequences of 2K to 128K keys): the streaming form 5 us and
-// 1.75 for each row and tile of its keys (64 rows x 128K: 117 us), the block form
-// 13 us and 9 for each tile of a block's run of rows (62 us; 8 rows x 128K: 17
-// against 19, 64 rows x 2K: 14 against 8).
+// 1024 rows of 1 and 4 sequences of 2K to 128K keys): the streaming form 5 us and
+// 1.75 for each row and tile of its keys (64 rows x 128K: 115 us), the block form
+// 13 us and 9 for each tile of a block's run of rows (46 us; 8 rows x 128K: 20
+// against 19, 64 rows x 2K: 15 against 8).
 bool use_blocks(int64_t n_rows, int64_t n_seq, int64_t max_len) {
   const int64_t tiles = (max_len + kTile - 1) / kTile;
-  const int64_t runs = (n_rows + kRows - 1) / kRows + min64(n_seq, n_rows) - 1;
-  return 4 * 8000 + 4 * 9 * runs * tiles < 7 * n_rows * tiles;
+  return 4 * 8000 + 4 * 9 * most_runs(n_rows, n_seq) * tiles < 7 * n_rows * tiles;
 }
 
 int sm_count() {
@@ -823,7 +837,7 @@ bool query_map(CUtensorMap* m, const void* base, int64_t n) {
   if (!fn) return false;
   const cuuint64_t dims[2] = {kDi, (cuuint64_t)n};
   const cuuint64_t strides[1] = {kDi};
-  const cuuint32_t box[2] = {kDi, 256}, step[2] = {1, 1};
+  const cuuint32_t box[2] = {kDi, 128}, step[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, step,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -862,7 +876,7 @@ cudaError_t launch_blocks(const Fp8IndexArgs& a, const CUtensorMap& map, cudaStr
   e = set_smem(fp8_index_block_kernel, (int)sizeof(BlockSmem), done);
   if (e != cudaSuccess) return e;
   // A CTA's start costs about four tiles: a share is no smaller.
-  const int64_t tiles = (n_rows + kRows - 1) / kRows * ((a.rows.max_len + kTile - 1) / kTile);
+  const int64_t tiles = most_runs(n_rows, a.rows.n_seq) * ((a.rows.max_len + kTile - 1) / kTile);
   const unsigned ctas = (unsigned)max64(1, min64(sm_count(), tiles / 4));
   e = launch_pdl(fp8_index_block_kernel, dim3(ctas), dim3(kBlkThreads), sizeof(BlockSmem), st, map, map_q, a,
                  (const float*)wq, (const int*)block_tiles);
