@@ -93,13 +93,13 @@ __device__ __forceinline__ PagedGeom paged_geom(const PagedRows& a, int r, bool 
   g.pad = false;
   g.nvis = 0;
   g.seq = a.seq_of_row ? a.seq_of_row[r] : r;
+  const int p = a.pos[r];  // asked for together with the sequence
   if (g.seq < 0 || g.seq >= a.n_seq) {
     g.pad = g.seq == -1;
     if (report && !g.pad) flag_error(a.err, LSA_DEVERR_SEQ);
     g.seq = -1;
     return g;
   }
-  const int p = a.pos[r];
   const int64_t room = min64(a.max_len, (int64_t)a.max_pages * kPage);
   g.nvis = (int64_t)p + 1;
   if (p < 0 || g.nvis > room) {

@@ -203,17 +203,23 @@ __device__ __forceinline__ void prefetch_q(const uint4* src, int lane) {
   if (lane < 4) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(src + (32 + lane) * 8));
 }
 
-// Returns the factor of the codes' products: one power of two for all heads of
-// the row (a logit's error counts absolutely) times the softmax's; NaN for a
-// query with an infinity or NaN.
-__device__ __forceinline__ float prepare_q(const Fp8MlaArgs& a, Fp8MlaSmem& sm, const uint4* src, uint32_t nk, int warp,
-                                           int lane) {
-  uint4 v[kQHeads][3];
+struct Query {
+  uint4 v[kQHeads][3];  // of the warp's heads, 8 elements a lane and third
+};
+__device__ __forceinline__ void load_q(Query& q, const uint4* src, int lane) {
 #pragma unroll
   for (int j = 0; j < kQHeads; ++j)
 #pragma unroll
     for (int c = 0; c < 3; ++c)
-      v[j][c] = lane + 32 * c < 72 ? __ldg(src + j * 72 + lane + 32 * c) : make_uint4(0, 0, 0, 0);
+      q.v[j][c] = lane + 32 * c < 72 ? __ldg(src + j * 72 + lane + 32 * c) : make_uint4(0, 0, 0, 0);
+}
+
+// Returns the factor of the codes' products: one power of two for all heads of
+// the row (a logit's error counts absolutely) times the softmax's; NaN for a
+// query with an infinity or NaN.
+__device__ __forceinline__ float prepare_q(const Fp8MlaArgs& a, Fp8MlaSmem& sm, const Query& q, uint32_t nk, int warp,
+                                           int lane) {
+  const auto& v = q.v;
   uint32_t m = 0;
 #pragma unroll
   for (int j = 0; j < kQHeads; ++j)
@@ -608,10 +614,14 @@ __device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& s
     }
   };
   if (i < sp.n_items) prefetch_q(query_of(a, sp, i, warp), lane);
-  find();
-  float qf = 0.f;  // the query's factor
-  if (i < sp.n_items) qf = prepare_q(a, sm, query_of(a, sp, i, warp), nk, warp, lane);
   while (i < sp.n_items) {
+    Query q;
+    load_q(q, query_of(a, sp, i, warp), lane);  // under way while the item is looked up
+    const int first = i;
+    find();
+    if (i >= sp.n_items) break;
+    if (i != first) load_q(q, query_of(a, sp, i, warp), lane);
+    const float qf = prepare_q(a, sm, q, nk, warp, lane);  // the query's factor
     if (i + (int)gridDim.x < sp.n_items) prefetch_q(query_of(a, sp, i + gridDim.x, warp), lane);
     float L[kHG];
 #pragma unroll
@@ -739,8 +749,6 @@ __device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& s
     }
     ++nk;
     i += gridDim.x;
-    find();
-    if (i < sp.n_items) qf = prepare_q(a, sm, query_of(a, sp, i, warp), nk, warp, lane);
   }
 }
 
