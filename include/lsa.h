@@ -592,7 +592,8 @@ LSA_API lsa_status lsa_fp8_sparse_mla(const lsa_config* cfg, int32_t n_sub, int3
  * key_pages may be NULL) and every sub-block is dense. Rows are processed in
  * blocks that fit the workspace (lsa_workspace_size(LSA_OP_FP8_FORWARD); the
  * minimum is one row's). idx_out int32 [n_rows, index_topk] and count_out int32
- * [n_rows]: optional (both or neither); unwritten when dense.
+ * [n_rows]: optional (both or neither); unwritten when dense; -1 and 0 for a row
+ * without a sequence.
  */
 LSA_API lsa_status lsa_fp8_forward(const lsa_config* cfg, int32_t n_rows, int32_t n_seq, const int32_t* seq_of_row,
                                    const int32_t* pos, int64_t max_len, const lsa_bf16* q_idx, const float* w,

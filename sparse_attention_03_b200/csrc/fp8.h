@@ -52,6 +52,7 @@ struct Fp8IndexArgs {
   float* scores;
   int64_t ld;
   uint32_t* hist;  // top-k histograms (zeroed by the launcher), or null
+  int32_t* top_pos;  // or null: gets the rows' last visible key for the top-k, -1 for a row without keys
   void* ws;        // fp8_index_ws_bytes, 256-byte aligned
 };
 size_t fp8_index_ws_bytes(int n_rows);

@@ -11,7 +11,7 @@ namespace {
 
 // Regions of one block of R rows of lsa_fp8_forward.
 struct ForwardPlan {
-  size_t scores, hist, idx, count, index, topk, mla, total;
+  size_t scores, hist, idx, count, pos, index, topk, mla, total;
   size_t topk_bytes, mla_bytes;
 };
 
@@ -27,6 +27,7 @@ ForwardPlan forward_plan(const lsa_config* c, int R, int64_t max_len) {
   p.hist = take((size_t)R * kTopkHistStride * sizeof(uint32_t));
   p.idx = take((size_t)R * c->index_topk * sizeof(int32_t));
   p.count = take((size_t)R * sizeof(int32_t));
+  p.pos = take((size_t)R * sizeof(int32_t));
   p.index = take(fp8_index_ws_bytes(R));
   p.topk_bytes = topk_ws(R, max_len);
   p.topk = take(p.topk_bytes);
@@ -197,6 +198,7 @@ lsa_status lsa_fp8_index_scores(const lsa_config* c, int32_t n_rows, int32_t n_s
   a.scores = scores;
   a.ld = ld;
   a.hist = topk_hist;
+  a.top_pos = nullptr;
   a.ws = base;
   return cuda_status(launch_fp8_index(a, (cudaStream_t)stream), fn);
 }
@@ -287,12 +289,13 @@ lsa_status lsa_fp8_forward(const lsa_config* c, int32_t n_rows, int32_t n_seq, c
     const bool hist = fp8_index_streams(nr, rows.n_seq, max_len) &&
                       max_len - c->index_init_tokens - c->index_local_tokens > kTopkShortMid;
     a.hist = hist ? reinterpret_cast<uint32_t*>(base + p.hist) : nullptr;
+    a.top_pos = reinterpret_cast<int32_t*>(base + p.pos);  // a padding row selects nothing, whatever its position says
     a.ws = base + p.index;
     s = cuda_status(launch_fp8_index(a, st), fn);
     if (s != LSA_OK) return s;
     int32_t* idx = idx_out ? idx_out + (int64_t)r0 * c->index_topk : reinterpret_cast<int32_t*>(base + p.idx);
     int32_t* count = count_out ? count_out + r0 : reinterpret_cast<int32_t*>(base + p.count);
-    s = run_topk(c, nr, rows.pos, max_len, a.scores, max_len, idx, count, base + p.topk, p.topk_bytes, st,
+    s = run_topk(c, nr, a.top_pos, max_len, a.scores, max_len, idx, count, base + p.topk, p.topk_bytes, st,
                  a.hist);
     if (s != LSA_OK) return s;
     Fp8MlaArgs m = {};

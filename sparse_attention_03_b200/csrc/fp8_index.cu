@@ -141,8 +141,8 @@ struct __align__(1024) DecodeSmem {
   uint32_t hist[2048];
 };
 
-__device__ __forceinline__ int64_t row_tiles(const PagedRows& rows, int r, bool report) {
-  return (paged_geom(rows, r, report).nvis + kTile - 1) / kTile;
+__device__ __forceinline__ int64_t row_tiles(const PagedRows& rows, int r) {
+  return (paged_geom(rows, r, false).nvis + kTile - 1) / kTile;
 }
 
 // The four epilogue warps' barrier with an OR.
@@ -211,7 +211,11 @@ __global__ void __launch_bounds__(kDecThreads, 2)
   const int n_rows = a.rows.n_rows, per = (n_rows + kDecThreads - 1) / kDecThreads;
   const int r0 = min(tid * per, n_rows), r1 = min(r0 + per, n_rows);
   unsigned long long mine = 0;
-  for (int r = r0; r < r1; ++r) mine += (unsigned long long)row_tiles(a.rows, r, blockIdx.x == 0);
+  for (int r = r0; r < r1; ++r) {
+    const int64_t nvis = paged_geom(a.rows, r, blockIdx.x == 0).nvis;
+    if (a.top_pos && blockIdx.x == 0) a.top_pos[r] = (int)(nvis - 1);
+    mine += (unsigned long long)((nvis + kTile - 1) / kTile);
+  }
   sm.sums[tid] = mine;
   __syncthreads();
   if (warp == 0) {  // exclusive prefix over the 320 threads, ten a lane
@@ -240,7 +244,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
   if (first < last && first >= before && first < before + mine) {
     unsigned long long at = before;
     for (int r = r0; r < r1; ++r) {
-      const unsigned long long n = (unsigned long long)row_tiles(a.rows, r, false);
+      const unsigned long long n = (unsigned long long)row_tiles(a.rows, r);
       if (first < at + n) {
         sm.start_row = r;
         sm.start_tile = (int)(first - at);
@@ -495,6 +499,7 @@ __global__ void __launch_bounds__(256) fp8_index_query_kernel(const __grid_const
       if (r < a.rows.n_rows) g = paged_geom(a.rows, r, true);
       seq[threadIdx.x] = g.seq;
       nvis[threadIdx.x] = g.nvis;
+      if (a.top_pos && r < a.rows.n_rows) a.top_pos[r] = (int)(g.nvis - 1);
     }
     __syncwarp();
     if (threadIdx.x == 0) {

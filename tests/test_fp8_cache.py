@@ -540,10 +540,10 @@ def _check_hist(rows, scores, h, cfg):
 
 
 @gpu
-@pytest.mark.parametrize("bound", [None, 60000])
+@pytest.mark.parametrize("bound", [None, 60000, 60001])
 def test_scores_of_prompt_rows_with_the_histogram(bound):
     lens = [300, 150]
-    rows = [(s, p) for s, n in enumerate(lens) for p in range(n - 40, n)]
+    rows = [(s, p) for s, n in enumerate(lens) for p in range(n - 40, n)] + [(-1, -1)] * 3
     cfg = lsa.LsaConfig(**TINY)
     err, scores, pos, h, _ = _score_case(lens, rows, cfg, hist=True, max_len=bound)
     assert err == 0
@@ -986,6 +986,106 @@ def test_serving_run_from_plan_to_layer():
                 tol, ltol = _mla_tol(_vals(q[z])[r], c, cs, sel, wt, o, cfg.softmax_scale)
                 assert (np.abs(lse[z][r].double().cpu().numpy() - l) <= ltol).all()
                 assert (np.abs(_vals(out[z])[r] - o) <= tol).all()
+
+
+@gpu
+@pytest.mark.parametrize("max_len", [300, 60000])     # the indexer's two forms
+def test_captured_layer_follows_its_inputs(max_len):
+    # lengths, sequences and pages change in place between replays; every replay is a call on what stands there
+    cfg = lsa.LsaConfig(index_topk=96, index_init_tokens=4, index_local_tokens=16)
+    c = Caches([300, 260], 41, cli=2)
+    n = 66
+    rng = np.random.default_rng(42)
+    q_idx, w, q, out, lse = _layer_inputs(rng, n)
+    table = torch.full_like(c.block_table, -1)
+    seq, pos = torch.full((n,), -1, dtype=torch.int32, device="cuda"), torch.zeros(n, dtype=torch.int32, device="cuda")
+    idx = torch.zeros(n, 96, dtype=torch.int32, device="cuda")
+    cnt = torch.zeros(n, dtype=torch.int32, device="cuda")
+    ws = lsa.workspace(cfg, lsa.OP_FP8_FORWARD, n, 2, max_len)
+
+    def layer():
+        lsa.fp8_forward(cfg, seq, pos, max_len, q_idx, w, c.key_pages, q, c.latent_pages, table, out, lse, ws, idx_out=idx,
+                        count_out=cnt)
+
+    layer()                                              # all padding
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        layer()
+    for step in range(3):
+        s = np.sort(rng.integers(-1, 2, n))[::-1].copy()
+        p = np.array([rng.integers(0, c.lens[k]) if k >= 0 else -1 for k in s])
+        seq.copy_(_i32(s)); pos.copy_(_i32(p)); table.copy_(c.block_table)
+        idx.fill_(-9)
+        g.replay()
+        assert lsa.device_error() == 0
+        got, got_idx = [o.clone() for o in out], idx.clone()
+        layer()
+        assert lsa.device_error() == 0
+        assert torch.equal(got_idx.sort(dim=1).values, idx.sort(dim=1).values)
+        for r in range(n):
+            assert int(cnt[r]) == (min(p[r] + 1, 96) if s[r] >= 0 else 0)
+            if torch.equal(got_idx[r], idx[r]):          # sums in the same order: the same bits
+                assert all(torch.equal(a[r], b[r]) for a, b in zip(got, out))
+    del g
+
+
+@gpu
+def test_two_calls_at_once_on_two_streams():
+    cfg = lsa.LsaConfig(index_topk=96, index_init_tokens=4, index_local_tokens=16)
+    calls = []
+    for k, (n, max_len) in enumerate([(66, 60000), (3, 900)]):
+        c = Caches([300, 900], 51 + k, cli=2)
+        rng = np.random.default_rng(61 + k)
+        q_idx, w, q, out, lse = _layer_inputs(rng, n)
+        seq, pos = _i32(np.arange(n) % 2), _i32(rng.integers(100, 300, n))
+        idx, cnt = torch.zeros(n, 96, dtype=torch.int32, device="cuda"), torch.zeros(n, dtype=torch.int32, device="cuda")
+        ws = lsa.workspace(cfg, lsa.OP_FP8_FORWARD, n, 2, max_len)
+        calls.append((lambda st, a=(cfg, seq, pos, max_len, q_idx, w, c.key_pages, q, c.latent_pages, c.block_table, out,
+                                    lse, ws), i=idx, t=cnt: lsa.fp8_forward(*a, idx_out=i, count_out=t, stream=st), out, idx))
+    want = []
+    for f, out, idx in calls:
+        f(None)
+        torch.cuda.synchronize()
+        want.append(([o.clone() for o in out], idx.clone()))
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(5):
+        for (f, out, idx), st in zip(calls, streams):
+            f(st)
+    torch.cuda.synchronize()
+    assert lsa.device_error() == 0
+    for (f, out, idx), (o0, i0) in zip(calls, want):
+        assert torch.equal(idx.sort(dim=1).values, i0.sort(dim=1).values)
+        for r in range(idx.shape[0]):
+            if torch.equal(idx[r], i0[r]):
+                assert all(torch.equal(a[r], b[r]) for a, b in zip(out, o0))
+
+
+@gpu
+@pytest.mark.parametrize("max_len", [300, 60000])     # the indexer's two forms
+def test_forward_padding_rows_with_any_position_select_nothing(max_len):
+    rng = np.random.default_rng(31)
+    cfg = lsa.LsaConfig(index_topk=96, index_init_tokens=4, index_local_tokens=16)
+    c = Caches([300], 32, cli=2)
+    n = 70
+    seq, pos = np.zeros(n, dtype=np.int64), 230 + np.arange(n)
+    seq[[0, 20, 21, 69]], seq[40] = -1, 9            # padding rows with positions that look real; an unknown sequence
+    q_idx, w, q, out, lse = _layer_inputs(rng, n)
+    for o in out:
+        o.fill_(9.0)
+    idx = torch.full((n, 96), -7, dtype=torch.int32, device="cuda")
+    cnt = torch.full((n,), -7, dtype=torch.int32, device="cuda")
+    ws = lsa.workspace(cfg, lsa.OP_FP8_FORWARD, n, 1, max_len)
+    lsa.fp8_forward(cfg, _i32(seq), _i32(pos), max_len, q_idx, w, c.key_pages, q, c.latent_pages, c.block_table, out,
+                    lse, ws, idx_out=idx, count_out=cnt)
+    assert lsa.device_error() == lsa.DEVERR_SEQ
+    for r in range(n):
+        if seq[r] != 0:
+            assert int(cnt[r]) == 0 and (idx[r] == -1).all()
+            assert (out[0][r] == (9.0 if seq[r] == -1 else 0.0)).all()
+        else:
+            assert int(cnt[r]) == 96 and len(set(idx[r].tolist())) == 96 and 0 <= int(idx[r].min()) <= int(idx[r].max()) <= pos[r]
+            assert torch.isfinite(out[0][r]).all() and not (out[0][r] == 9.0).all()
 
 
 @gpu
