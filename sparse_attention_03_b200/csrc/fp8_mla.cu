@@ -603,26 +603,29 @@ __device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& s
   float4* frame = sm.frame[warp];
   Frames f;
   uint32_t g = 0, nk = 0;
-  // The next item from `i` on that has tiles.
-  int i = blockIdx.x, t0 = 0, t1 = 0;
-  auto find = [&]() {
-    for (; i < sp.n_items; i += gridDim.x) {
-      const Item it = load_item(a, sp, i, false);
-      t0 = it.t0;
-      t1 = it.t1;
-      if (t0 < t1) break;
-    }
+  // The first item from `from` on that has tiles.
+  struct Work {
+    int i, t0, t1;
   };
-  if (i < sp.n_items) prefetch_q(query_of(a, sp, i, warp), lane);
-  while (i < sp.n_items) {
+  auto find = [&](int from) {
+    Work w = {from, 0, 0};
+    for (; w.i < sp.n_items; w.i += gridDim.x) {
+      const Item it = load_item(a, sp, w.i, false);
+      w.t0 = it.t0;
+      w.t1 = it.t1;
+      if (w.t0 < w.t1) break;
+    }
+    return w;
+  };
+  if ((int)blockIdx.x < sp.n_items) prefetch_q(query_of(a, sp, blockIdx.x, warp), lane);
+  Work cur = find(blockIdx.x);
+  while (cur.i < sp.n_items) {
     Query q;
-    load_q(q, query_of(a, sp, i, warp), lane);  // under way while the item is looked up
-    const int first = i;
-    find();
-    if (i >= sp.n_items) break;
-    if (i != first) load_q(q, query_of(a, sp, i, warp), lane);
+    load_q(q, query_of(a, sp, cur.i, warp), lane);
     const float qf = prepare_q(a, sm, q, nk, warp, lane);  // the query's factor
-    if (i + (int)gridDim.x < sp.n_items) prefetch_q(query_of(a, sp, i + gridDim.x, warp), lane);
+    const Work next = find(cur.i + gridDim.x);             // looked up while the first tile's products run
+    if (next.i < sp.n_items) prefetch_q(query_of(a, sp, next.i, warp), lane);
+    const int t0 = cur.t0, t1 = cur.t1;
     float L[kHG];
 #pragma unroll
     for (int j = 0; j < kHG; ++j) L[j] = f.m[j] = f.w[j] = 0.f;
@@ -650,7 +653,7 @@ __device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& s
       bool force = anew || !framed || !ok, moved = false;
       while (true) {
         if (!force) weights(s_addr, f, valid, sq, su, p, u, top_p, top_u);
-        if (!softmax_any(group, force || (!moved && (top_u > 128.f || top_p > 0x1p60f)))) break;
+        if (moved || !softmax_any(group, force || top_u > 128.f || top_p > 0x1p60f)) break;
         force = false;
         moved = true;
         // Set the frames from this tile's maxima (the group's four warps, the same values).
@@ -748,7 +751,7 @@ __device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& s
       if (lane == 0) mbar_arrive(&sm.fin_full[f]);
     }
     ++nk;
-    i += gridDim.x;
+    cur = next;
   }
 }
 
