@@ -21,6 +21,9 @@ current stream, checks the device error flags and exits. Cases:
                  lsa_sparse_mla_prefill for two sub-blocks
   hier_decode    lsa_block_summaries of each row's newest block + lsa_hier_select (64-key blocks,
                  128 kept), 16 rows x 131072 keys
+  fp8_append     lsa_fp8_append, 16384 rows (2 sub-blocks and the index key)
+  fp8_decode     lsa_fp8_index_scores with the top-k histogram, 16 rows x 131072 paged 8-bit keys
+  fp8_chunk      lsa_fp8_forward (cli 2), 1024 rows at the end of 16384 paged 8-bit keys
 """
 from __future__ import annotations
 
@@ -205,6 +208,56 @@ def case_hier_decode(reps):
         lsa.block_summaries(cfg, new_seq, new_blk, wl.k_idx, wl.k_off, blk_off, k_blk, block)
         lsa.hier_select(cfg, wl.seq_of_row, wl.pos, wl.q_idx, wl.w, wl.k_idx, wl.k_off, k_blk, blk_off, ctx, idx,
                         cnt, ws, block, n_blocks)
+
+
+class _Paged:
+    """Sequences of one length in paged 8-bit caches, through the page plan and the append."""
+
+    def __init__(self, n_seq, length, cli):
+        self.cfg, n, width = lsa.LsaConfig(), n_seq * length, -(-length // lsa.PAGE_TOKENS)
+        n_pages = n_seq * width
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+        free = torch.randperm(n_pages, device="cuda", generator=torch.Generator("cuda").manual_seed(0)).int()
+        self.table = torch.full((n_seq, width), -1, dtype=torch.int32, device="cuda")
+        self.seq, self.pos, self.slot = (torch.empty(n, dtype=torch.int32, device="cuda") for _ in range(3))
+        lsa.page_plan(i32([0] * n_seq), i32([length] * n_seq), free, self.table, self.seq, self.pos, self.slot,
+                      torch.empty(2, dtype=torch.int32, device="cuda"))
+        self.keys, self.latent = lsa.key_pages(n_pages), [lsa.latent_pages(n_pages) for _ in range(cli)]
+        self.rows = [torch.randn(n, 576, device="cuda", dtype=torch.bfloat16) for _ in range(cli)]
+        self.k = torch.randn(n, 128, device="cuda", dtype=torch.bfloat16)
+        self.append()
+
+    def append(self):
+        lsa.fp8_append(self.cfg, self.slot, self.rows, self.latent, self.k, self.keys)
+
+
+def case_fp8_append(reps):
+    c = _Paged(1, 16384, 2)
+    for _ in range(reps):
+        c.append()
+
+
+def case_fp8_decode(reps):
+    n, L = 16, 131072
+    c = _Paged(n, L, 0)
+    pos = torch.full((n,), L - 1, dtype=torch.int32, device="cuda")
+    q, w = torch.randn(n, 32, 128, device="cuda", dtype=torch.bfloat16), torch.randn(n, 32, device="cuda")
+    scores, hist = torch.empty(n, L, device="cuda"), lsa.topk_hist_buffer(n)
+    ws = lsa.workspace(c.cfg, lsa.OP_FP8_INDEX, n, n, L)
+    for _ in range(reps):
+        lsa.fp8_index_scores(c.cfg, None, pos, q, w, c.keys, c.table, L, scores, ws, topk_hist=hist)
+
+
+def case_fp8_chunk(reps):
+    n, L = 1024, 16384
+    c = _Paged(1, L, 2)
+    seq, pos = c.seq[-n:].contiguous(), c.pos[-n:].contiguous()
+    q, w = torch.randn(n, 32, 128, device="cuda", dtype=torch.bfloat16), torch.randn(n, 32, device="cuda")
+    q_abs = [torch.randn(n, 32, 576, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    out = [torch.empty(n, 32, 512, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    ws = lsa.workspace(c.cfg, lsa.OP_FP8_FORWARD, n, 1, L)
+    for _ in range(reps):
+        lsa.fp8_forward(c.cfg, seq, pos, L, q, w, c.keys, q_abs, c.latent, c.table, out, None, ws)
 
 
 CASES = {name[5:]: fn for name, fn in globals().items() if name.startswith("case_")}
