@@ -13,8 +13,8 @@
 // key against 180 of ~730 cycles a 128-key tile for the products (16 x 128K keys:
 // 49 us, 5.8 TB/s; 64 x 16K to 32K: 38 us; one row x 8K: 5 us, latency). Rows that
 // share their keys (a prompt's chunk) are bound by the tensor cores and the
-// ReLU-weighted sum over them: 16 rows a CTA, N = 256. The host takes the form
-// that costs less (use_blocks).
+// ReLU-weighted sum over them: 16 rows at a time, N = 128 (4 rows x 32 heads). The
+// host takes the form that costs less (use_blocks).
 //
 // A tile is two pages of 64 keys, each one TMA copy of 8 KB (the 128-byte
 // swizzle) and one bulk copy of its 64 scales into a ring of their own (the
@@ -462,7 +462,7 @@ struct __align__(1024) BlockSmem {
   int seq[kRows];
   // runs of rows of one sequence: its rows [run_r0, run_r1) of the block, its tiles
   int run_r0[kRows], run_r1[kRows], run_tiles[kRows], n_runs;
-  long long sums[kEpiWarps + 2], total;
+  long long sums[kEpiWarps + 2];
   int start_block, start_tile;
   uint64_t full[kBStages], empty[kBStages], tfull[kGroups], tempty[kGroups], qfull;
   uint32_t tmem_base;
