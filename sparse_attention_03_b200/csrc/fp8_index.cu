@@ -449,8 +449,8 @@ constexpr int kBStages = 6;
 constexpr int kEpiWarps = 16;
 constexpr int kGroups = 4;                    // accumulators of 128 columns: 4 rows x 32 heads, four warps each
 static_assert(kRows / kEpiWarps == 1, "a warp sums four rows of a quarter of the keys");
-constexpr int kProducer = kEpiWarps, kMma = kEpiWarps + 1;  // their warps
-constexpr int kBlkThreads = (kEpiWarps + 2) * 32;
+constexpr int kProducer = kEpiWarps, kMma = kEpiWarps + 1;  // their warps (the products': two)
+constexpr int kBlkWarps = kEpiWarps + 3, kBlkThreads = kBlkWarps * 32;
 constexpr uint32_t kGroupBytes = 128 * kDi;   // 4 rows x 32 heads x 128 codes: 16 KB
 
 struct __align__(1024) BlockSmem {
@@ -460,32 +460,33 @@ struct __align__(1024) BlockSmem {
   __align__(16) float w[kRows][kHi];
   int64_t nvis[kRows];
   int seq[kRows];
-  // runs of rows of one sequence: its rows [run_r0, run_r1) of the block, its tiles
-  int run_r0[kRows], run_r1[kRows], run_tiles[kRows], n_runs;
-  long long sums[kEpiWarps + 2];
-  int start_block, start_tile;
+  // runs of rows of one sequence: its rows [run_r0, run_r1) of the block, its tiles, the cost of one
+  int run_r0[kRows], run_r1[kRows], run_tiles[kRows], run_cost[kRows], n_runs;
+  long long sums[kBlkWarps], start_at;
+  int start_block;
   uint64_t full[kBStages], empty[kBStages], tfull[kGroups], tempty[kGroups], qfull;
   uint32_t tmem_base;
   int abort_flag;
 };
 
 // The tiles that a block of rows takes: the runs of rows of one sequence, each up to
-// its furthest visible key. seq[i], nvis[i]: row i's sequence (-1: none) and keys.
+// its furthest visible key. A tile costs its load and the groups of four rows that
+// the run has a part in. seq[i], nvis[i]: row i's sequence (-1: none) and keys.
 template <typename F>
 __device__ __forceinline__ void block_runs(const int* seq, const int64_t* nvis, F&& run) {
   for (int i = 0; i < kRows;) {
     int e = i + 1;
     int64_t most = nvis[i];
     for (; e < kRows && seq[e] == seq[i]; ++e) most = max64(most, nvis[e]);
-    if (seq[i] >= 0 && most > 0) run(i, e, (int)((most + kTile - 1) / kTile));
+    if (seq[i] >= 0 && most > 0) run(i, e, (int)((most + kTile - 1) / kTile), 2 + (e - 1) / 4 - i / 4);
     i = e;
   }
 }
 
-// The codes and weights of all rows' queries, a half warp a head, and every block's
-// tiles (a CTA has the 16 heads of half a row: every 32nd takes a block).
+// The codes and weights of all rows' queries, a half warp a head, and the cost of
+// every block's tiles (a CTA has the 16 heads of half a row: every 32nd takes a block).
 __global__ void __launch_bounds__(256) fp8_index_query_kernel(const __grid_constant__ Fp8IndexArgs a, uint8_t* codes,
-                                                              float* wq, int* block_tiles) {
+                                                              float* wq, int* block_cost) {
   pdl_wait();
   const int64_t head = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 4;
   const int sub = threadIdx.x & 15;
@@ -505,8 +506,8 @@ __global__ void __launch_bounds__(256) fp8_index_query_kernel(const __grid_const
     __syncwarp();
     if (threadIdx.x == 0) {
       int n = 0;
-      block_runs(seq, nvis, [&](int, int, int tiles) { n += tiles; });
-      block_tiles[block] = n;
+      block_runs(seq, nvis, [&](int, int, int tiles, int cost) { n += tiles * cost; });
+      block_cost[block] = n;
     }
     __syncwarp();
   }
@@ -534,14 +535,27 @@ struct RunCursor {
   }
 };
 
+// How many of the block's tiles begin before cost x (from the block's begin).
+__device__ __forceinline__ int tiles_before(const BlockSmem& sm, long long x) {
+  int n = 0;
+  for (int r = 0; r < sm.n_runs && x > 0; ++r) {
+    const int cost = sm.run_cost[r], all = sm.run_tiles[r] * cost;
+    n += x >= all ? sm.run_tiles[r] : ((int)x + cost - 1) / cost;
+    x -= all;
+  }
+  return n;
+}
+
 // Persistent: the tiles of all blocks of 16 rows (the furthest rows' block first)
-// make one list, of which every CTA takes an equal share, block after block. Warps:
-// sixteen for the epilogue, TMA producer, MMA. A tile's products are four
+// make one list, of which every CTA takes an equal share (by cost), block after
+// block. Warps: sixteen for the epilogue, TMA producer, two for the products (with
+// one, the issue and its waits held them: 302 us). A tile's products are four
 // accumulators of 4 rows x 32 heads, each with its own four epilogue warps (a thread
 // = a key), so a group's sums wait for nobody else's. Rows of several sequences (a
-// block that straddles prompts) take their sequences' tiles one after the other.
+// block that straddles prompts, or has a few rows of each) take their sequences'
+// tiles one after the other, with the groups that have a row of the sequence.
 //
-// 4096 rows x 16K keys: 269 us, 1.79 PFLOP/s. The products alone (no sums, no
+// 4096 rows x 16K keys: 277 us, 1.73 PFLOP/s. The products alone (no sums, no
 // stores) run in 180; the sums (a maximum a product, an FMA for two, eight loads of
 // weights a row and key quarter: ~70 instructions, 16 rows a scheduler and tile)
 // need 1150 cycles a tile beside the products' 1030 and get 62% of the issue slots.
@@ -550,7 +564,7 @@ struct RunCursor {
 // (269), x + |x| for max(0, x) (272).
 __global__ void __launch_bounds__(kBlkThreads, 1)
     fp8_index_block_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap map_q,
-                           const __grid_constant__ Fp8IndexArgs a, const float* wq, const int* block_tiles) {
+                           const __grid_constant__ Fp8IndexArgs a, const float* wq, const int* block_cost) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   if ((smem_u32(smem_raw) & 1023u) != 0) {
     if (threadIdx.x == 0) flag_error(a.rows.err, LSA_DEVERR_TIMEOUT);
@@ -562,7 +576,7 @@ __global__ void __launch_bounds__(kBlkThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < kBStages; ++s) {
       mbar_init(&sm.full[s], 2);  // load_tile's two announcements
-      mbar_init(&sm.empty[s], 1);
+      mbar_init(&sm.empty[s], 2);  // both MMA warps
     }
     for (int b = 0; b < kGroups; ++b) {
       mbar_init(&sm.tfull[b], 2);  // the products' commit, and the MMA warp's own arrival
@@ -580,7 +594,7 @@ __global__ void __launch_bounds__(kBlkThreads, 1)
   const int per = (n_blocks + kBlkThreads - 1) / kBlkThreads;
   const int b0 = min(tid * per, n_blocks), b1 = min(b0 + per, n_blocks);  // places in the list
   long long part = 0;
-  for (int b = b0; b < b1; ++b) part += block_tiles[n_blocks - 1 - b];
+  for (int b = b0; b < b1; ++b) part += block_cost[n_blocks - 1 - b];
   long long before = part;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -593,33 +607,29 @@ __global__ void __launch_bounds__(kBlkThreads, 1)
   __syncthreads();
   tc_fence_after();
   long long total = 0;
-  for (int i = 0; i < kEpiWarps + 2; ++i) {
+  for (int i = 0; i < kBlkWarps; ++i) {
     if (i == warp) before += total;
     total += sm.sums[i];
   }
   const long long lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
   if (lo < hi && before <= lo && lo < before + part) {
     int b = b0;
-    for (long long at = before;; ++b) {
-      const int n = block_tiles[n_blocks - 1 - b];
-      if (lo < at + n) {
-        sm.start_tile = (int)(lo - at);
-        break;
-      }
-      at += n;
-    }
+    long long at = before;
+    for (; lo >= at + block_cost[n_blocks - 1 - b]; ++b) at += block_cost[n_blocks - 1 - b];
+    sm.start_at = at;
     sm.start_block = n_blocks - 1 - b;
   }
   __syncthreads();
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort_flag = &sm.abort_flag;
-  int block = sm.start_block, first_tile = sm.start_tile;
-  long long left = hi - lo;
-  uint32_t g = 0;  // tiles of the CTA before this block's
+  int block = sm.start_block;
+  uint32_t g = 0;       // tiles of the CTA before this block's
+  uint32_t turns = 0;   // parity of the warp's uses of an accumulator (an MMA warp: a bit for each of two)
+  if (lo >= hi) block = -1;
 
-  for (uint32_t seg = 0; left > 0; --block, first_tile = 0) {
-    const int n_tiles = (int)min64(block_tiles[block] - first_tile, left);
-    if (n_tiles == 0) continue;  // padding
+  uint32_t seg = 0;
+  for (long long at = sm.start_at; block >= 0 && at < hi; at += block_cost[block--]) {
+    if (block_cost[block] == 0) continue;  // padding
     const int row0 = block * kRows;
     if (tid < kRows) {
       PagedGeom geom = {-1, true, 0};
@@ -633,23 +643,30 @@ __global__ void __launch_bounds__(kBlkThreads, 1)
       __syncwarp();
       if (lane == 0) {
         int n = 0;
-        block_runs(sm.seq, sm.nvis, [&](int r0, int r1, int tiles) {
+        block_runs(sm.seq, sm.nvis, [&](int r0, int r1, int tiles, int cost) {
           sm.run_r0[n] = r0;
           sm.run_r1[n] = r1;
+          sm.run_cost[n] = cost;
           sm.run_tiles[n++] = tiles;
         });
         sm.n_runs = n;
       }
     }
-    if (warp == kProducer && lane == 0) {  // the last block's products have been read: the queries' place is free
-      mbar_expect_tx(&sm.qfull, kGroups * kGroupBytes);
-      for (int q = 0; q < kGroups; ++q) tma_load_2d(sm.b[q], &map_q, 0, row0 * kHi + q * 128, &sm.qfull);
-    }
     __syncthreads();
+    const int first_tile = tiles_before(sm, lo - at), n_tiles = tiles_before(sm, hi - at) - first_tile;
+    if (n_tiles == 0) {  // none begins in this share
+      __syncthreads();
+      continue;
+    }
     RunCursor cur;
     cur.start(sm, first_tile);
     if (warp == kProducer) {
       // ---------------- producer ----------------
+      if (lane == 0) {  // the last block's products have been read: the queries' place is free
+        mbar_expect_tx(&sm.qfull, kGroups * kGroupBytes);
+        for (int q = 0; q < kGroups; ++q) tma_load_2d(sm.b[q], &map_q, 0, row0 * kHi + q * 128, &sm.qfull);
+      }
+      __syncwarp();
       int pages = 0, batch_run = -1, batch = 0;
       int64_t most = 0;
       uint32_t i = g;
@@ -678,32 +695,56 @@ __global__ void __launch_bounds__(kBlkThreads, 1)
         while (!mbar_try_wait(&sm.qfull, seg & 1) && global_ns() - t_out < kWaitLimitNs) {
         }
       }
-    } else if (warp == kMma) {
+    } else if (warp >= kMma) {
       // ---------------- MMA ----------------
       const uint32_t leader = elect_one();
       bool ok = mbar_wait_fast(&sm.qfull, seg & 1, abort_flag);
-      for (uint32_t i = g; ok && i < g + n_tiles; ++i) {
+      const int q_first = (warp - kMma) * 2;  // its accumulators: this and the next
+      // The accumulator's last use, if any, has been read.
+      auto released = [&](int k) { return mbar_wait_fast(&sm.tempty[q_first + k], (turns >> k & 1) ^ 1, abort_flag); };
+      const uint64_t bd = sw128_desc(smem_u32(sm.b[q_first]));
+      int run = -1;
+      bool live[2] = {false, false};  // which of the two have rows of the run
+      for (uint32_t i = g; ok && i < g + n_tiles; ++i, cur.next(sm)) {
+        if (cur.run != run) {
+          // Both have been read, and with them the last run's scales (one without rows in
+          // this run holds nothing up from here on).
+          ok = released(0) && released(1);
+          if (!ok) break;
+          run = cur.run;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) live[k] = sm.run_r0[run] / 4 <= q_first + k && q_first + k <= (sm.run_r1[run] - 1) / 4;
+        }
         const int s = i % kBStages;
         if (!mbar_wait_fast(&sm.full[s], (i / kBStages) & 1, abort_flag)) break;
         const uint64_t ad = sw128_desc(smem_u32(sm.a[s]));
-        for (int q = 0; q < kGroups; ++q) {
-          if (i > 0 && !mbar_wait_fast(&sm.tempty[q], (i - 1) & 1, abort_flag)) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (!live[k]) continue;
+          if (!released(k)) {
             ok = false;
             break;
           }
           __syncwarp();
           tc_fence_after();
-          const uint64_t bd = sw128_desc(smem_u32(sm.b[q]));
+          const int q = q_first + k;
 #pragma unroll
           for (int c = 0; c < kDi / 32; ++c)
-            umma_f8(tmem + q * 128, ad + (c * 32 >> 4), bd + (c * 32 >> 4), f8_idesc(128, false), c > 0 ? 1u : 0u, leader);
+            umma_f8(tmem + q * 128, ad + (c * 32 >> 4), bd + ((k * kGroupBytes + c * 32) >> 4), f8_idesc(128, false),
+                    c > 0 ? 1u : 0u, leader);
           if (leader) {
             umma_commit(&sm.tfull[q]);
             mbar_arrive(&sm.tfull[q]);
-            if (q == kGroups - 1) umma_commit(&sm.empty[s]);
           }
+          turns ^= 1u << k;
           __syncwarp();
         }
+        if (!ok) break;
+        if (leader) {
+          if (live[0] || live[1]) umma_commit(&sm.empty[s]);
+          else mbar_arrive(&sm.empty[s]);
+        }
+        __syncwarp();
       }
     } else {
       // ---------------- epilogue ----------------
@@ -711,7 +752,7 @@ __global__ void __launch_bounds__(kBlkThreads, 1)
       const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + row_in * 32;
       const int lane_j = quarter * 32 + lane;
       const float(*wrow)[kHi] = sm.w + row_in;
-      float* o = a.scores + (int64_t)(row0 + row_in) * a.ld + (int64_t)cur.tile * kTile + lane_j;
+      float* o = nullptr;
       // Of a run: its tiles to come, the warp's rows in it, and the tiles [plain_lo,
       // plain_hi) whose keys are visible to all of the four and forced for none.
       int tiles_left = 0, mine = 0, plain_lo = 0, plain_hi = 0;
@@ -727,11 +768,20 @@ __global__ void __launch_bounds__(kBlkThreads, 1)
               most = min64(most, sm.nvis[row_in + u] - a.n_loc);
             }
           }
+          if (mine == 0) {  // no work in this run: on to the next
+            i += tiles_left - 1;
+            tiles_left = 0;
+            cur.tile = sm.run_tiles[cur.run] - 1;
+            cur.next(sm);
+            continue;
+          }
           plain_lo = (a.n_init + kTile - 1) / kTile;
           plain_hi = mine == 15 ? (int)(max64(most, 0) / kTile) : 0;
+          o = a.scores + (int64_t)(row0 + row_in) * a.ld + (int64_t)cur.tile * kTile + lane_j;
         }
         // What the MMA warp saw (the tile's scales in place) holds here too: it arrives on tfull as its commit does.
-        if (!mbar_wait_fast(&sm.tfull[group], i & 1, abort_flag)) break;
+        if (!mbar_wait_fast(&sm.tfull[group], turns & 1, abort_flag)) break;
+        turns ^= 1;
         __syncwarp();
         tc_fence_after();
         // A row at a time, its weights on the way with its products.
@@ -771,7 +821,6 @@ __global__ void __launch_bounds__(kBlkThreads, 1)
         if (--tiles_left == 0) {
           --cur.tile;
           cur.next(sm);
-          o = a.scores + (int64_t)(row0 + row_in) * a.ld + lane_j;
         }
       }
     }
@@ -780,7 +829,6 @@ __global__ void __launch_bounds__(kBlkThreads, 1)
     if (*abort_flag) break;
     ++seg;
     g += n_tiles;
-    left -= n_tiles;
   }
   tc_fence_before();
   __syncthreads();
@@ -794,14 +842,17 @@ __global__ void __launch_bounds__(kBlkThreads, 1)
 // The most runs of rows of one sequence that the blocks can have.
 int64_t most_runs(int64_t n_rows, int64_t n_seq) { return (n_rows + kRows - 1) / kRows + min64(n_seq, n_rows) - 1; }
 
-// The form that these rows take, by what the two cost here (ns, measured over 1 to
-// 1024 rows of 1 and 4 sequences of 2K to 128K keys): the streaming form 5 us and
-// 1.75 for each row and tile of its keys (64 rows x 128K: 115 us), the block form
-// 13 us and 9 for each tile of a block's run of rows (46 us; 8 rows x 128K: 20
-// against 19, 64 rows x 2K: 15 against 8).
+// The form that these rows take, by what the two cost here (ns; measured over 1 to
+// 1024 rows, 1 to 64 sequences, 1K to 128K keys), the rows taken to be spread evenly
+// over the sequences: the streaming form 5 us and 1.75 for each row and tile of its
+// keys, the block form 13 us and, for each tile of a run of rows, 3.5 and 1.3 for each
+// of its groups of four. Streaming against blocks (us): 64 rows of one sequence x
+// 128K 115, 48; 8 rows x 128K 19, 18; 64 rows x 2K 8, 16; 64 sequences x 32K of 2 rows
+// each 93, 110; of 4 rows 180, 98; of 8 rows 328, 115.
 bool use_blocks(int64_t n_rows, int64_t n_seq, int64_t max_len) {
-  const int64_t tiles = (max_len + kTile - 1) / kTile;
-  return 4 * 8000 + 4 * 9 * most_runs(n_rows, n_seq) * tiles < 7 * n_rows * tiles;
+  const int64_t tiles = (max_len + kTile - 1) / kTile, seqs = max64(1, min64(n_seq, n_rows));
+  const int64_t each = (n_rows + seqs - 1) / seqs, runs = seqs * ((each + kRows - 1) / kRows), groups = seqs * ((each + 3) / 4);
+  return 20 * 8000 + (70 * runs + 26 * groups) * tiles < 35 * n_rows * tiles;
 }
 
 int sm_count() {
@@ -872,11 +923,11 @@ cudaError_t launch_blocks(const Fp8IndexArgs& a, const CUtensorMap& map, cudaStr
   const int n_rows = a.rows.n_rows;
   uint8_t* codes = static_cast<uint8_t*>(a.ws);
   float* wq = reinterpret_cast<float*>(codes + (size_t)n_rows * kHi * kDi);
-  int* block_tiles = reinterpret_cast<int*>(wq + (size_t)n_rows * kHi);
+  int* block_cost = reinterpret_cast<int*>(wq + (size_t)n_rows * kHi);
   CUtensorMap map_q;
   if (!query_map(&map_q, codes, (int64_t)n_rows * kHi)) return cudaErrorInvalidValue;
   cudaError_t e = launch_pdl(fp8_index_query_kernel, dim3((unsigned)(((int64_t)n_rows * kHi * 16 + 255) / 256)), dim3(256), 0,
-                             st, a, codes, wq, block_tiles);
+                             st, a, codes, wq, block_cost);
   count_launches(1);
   if (e != cudaSuccess) return e;
   e = set_smem(fp8_index_block_kernel, (int)sizeof(BlockSmem), done);
@@ -885,7 +936,7 @@ cudaError_t launch_blocks(const Fp8IndexArgs& a, const CUtensorMap& map, cudaStr
   const int64_t tiles = most_runs(n_rows, a.rows.n_seq) * ((a.rows.max_len + kTile - 1) / kTile);
   const unsigned ctas = (unsigned)max64(1, min64(sm_count(), tiles / 4));
   e = launch_pdl(fp8_index_block_kernel, dim3(ctas), dim3(kBlkThreads), sizeof(BlockSmem), st, map, map_q, a,
-                 (const float*)wq, (const int*)block_tiles);
+                 (const float*)wq, (const int*)block_cost);
   count_launches(1);
   if (e != cudaSuccess) return e;
   if (!a.hist) return cudaSuccess;

@@ -515,9 +515,10 @@ def test_scores_rows_without_a_map_are_the_sequences():
 
 
 @gpu
-@pytest.mark.parametrize("bound", [None, 60000])   # the bound on the lengths decides the kernel's form
+@pytest.mark.parametrize("bound", [None, 120000])  # the bound on the lengths decides the kernel's form
 @pytest.mark.parametrize("lens,new,pad", [([40], 40, 0), ([300], 37, 2), ([129, 700], 64, 5), ([17, 20, 260, 33], 17, 0),
-                                          ([1500], 129, 1)])
+                                          ([1500], 129, 1), ([300, 140, 64, 700] * 5, 4, 0), ([131, 260, 5, 400] * 5, 3, 0),
+                                          ([131, 260, 65, 400] * 4, 6, 3)])
 def test_scores_rows_of_prompts(lens, new, pad, bound):
     # many rows of few sequences (blocks of rows share key tiles; a block may span sequences and end in padding)
     rows = [(s, p) for s, n in enumerate(lens) for p in range(max(0, n - new), n)] + [(-1, -1)] * pad
