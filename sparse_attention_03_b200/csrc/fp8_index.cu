@@ -555,13 +555,11 @@ __device__ __forceinline__ int tiles_before(const BlockSmem& sm, long long x) {
 // block that straddles prompts, or has a few rows of each) take their sequences'
 // tiles one after the other, with the groups that have a row of the sequence.
 //
-// 4096 rows x 16K keys: 277 us, 1.73 PFLOP/s. The products alone (no sums, no
-// stores) run in 180; the sums (a maximum a product, an FMA for two, eight loads of
-// weights a row and key quarter: ~70 instructions, 16 rows a scheduler and tile)
-// need 1150 cycles a tile beside the products' 1030 and get 62% of the issue slots.
-// Measured and not kept: two accumulators of 256 columns (301), eight epilogue warps
-// with three rows in flight (365), half rows with the next half's load in flight
-// (269), x + |x| for max(0, x) (272).
+// 4096 rows x 16K keys: 277 us, 1.73 PFLOP/s. Without the sums and the stores 197;
+// the sums (a maximum a product, an FMA for two, eight loads of weights a row and key
+// quarter: ~70 instructions, 16 rows a scheduler and tile) need 1150 cycles a tile
+// beside the products' 1030 and get 64% of the issue slots. Accumulators of 256
+// columns took 301 us, eight epilogue warps 365, x + |x| for half of the maxima 291.
 __global__ void __launch_bounds__(kBlkThreads, 1)
     fp8_index_block_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap map_q,
                            const __grid_constant__ Fp8IndexArgs a, const float* wq, const int* block_cost) {
