@@ -582,7 +582,10 @@ __device__ __forceinline__ void mma_role(const Fp8MlaArgs& a, const Split& sp, F
 // frames (in registers: a shared load waits behind the gather's copies): p for
 // the sum, u = p s 2^(2 - A + m) for the product; S from tensor memory. `sq`: the
 // key's scale times the query's factor; `su`: the scale, or 0 for a key that adds
-// nothing to O.
+// nothing to O. The product of a large scale and a low frame's factor would
+// overflow beside a p of zero, so a scale above 1 goes to p and one below to the
+// factor: u is exact wherever it counts, and infinite or NaN only where p is (or
+// where u is above 128 and the frame is raised).
 struct Frames {
   float m[kHG], w[kHG];  // -m, 2^(2 - A + m)
 };
@@ -590,10 +593,11 @@ __device__ __forceinline__ void weights(uint32_t s_addr, const Frames& f, bool v
                                         float (&p)[kHG], float (&u)[kHG], float& top_p, float& top_u) {
   tmem_ld16_x2(s_addr, s_addr + kH, p, u);  // hi and lo
   top_p = top_u = 0.f;
+  const float s_up = fmaxf(su, 1.f), s_down = fminf(su, 1.f);
 #pragma unroll
   for (int h = 0; h < kHG; ++h) {
     p[h] = ex2(fmaf(fmaf(u[h], 0.0625f, p[h]), sq, f.m[h]));
-    u[h] = p[h] * (su * f.w[h]);
+    u[h] = (p[h] * s_up) * (s_down * f.w[h]);
     top_p = fmaxf(top_p, p[h]);
     top_u = fmaxf(top_u, u[h]);
   }
@@ -688,8 +692,9 @@ __device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& s
         const float m_old = m_h, a_old = a_h;
         if (tl > -INFINITY) m_h = framed ? fmaxf(m_old, tl + m_old) : tl + m_old;
         if (ta > -INFINITY) {
-          // down by at most 2^60 from the item's highest: O, scaled up by as much, stays far from overflow
-          d_h = ceilf(fmaxf(ta + m_old, anew ? a_top - 60.f : a_old) - m_h);
+          // down by at most 2^60 from the item's highest: O, scaled up by as much, stays far from overflow;
+          // and to no less than 2^-124 of m: the weights' factor and O's are then powers of two in range
+          d_h = fmaxf(ceilf(fmaxf(ta + m_old, anew ? a_top - 60.f : a_old) - m_h), -124.f);
           a_h = m_h + d_h;
           a_top = fmaxf(a_top, a_h);
         }

@@ -1123,3 +1123,69 @@ def test_forward_dense_small_workspace_and_split_rows():
         assert torch.equal(ix, got[0][1])
         for a, b in zip(o, got[0][0]):
             assert (a.float() - b.float()).abs().max() <= 2.0 ** -6 * b.float().abs().max()
+
+
+# ------------------------------------------------------------------ GPU: the attention's frames at their ends
+
+
+def _sequence(lat, seed=0):
+    """One sequence holding these latent rows (bf16 [n, 576]), put there by the append."""
+    n = len(lat)
+    c = Caches([n], seed, cli=1)
+    t = torch.arange(n, device="cuda")
+    slot = (torch.from_numpy(c.table[0]).cuda()[t // 64] * 64 + t % 64).int()
+    lsa.fp8_append(lsa.LsaConfig(cli_factor=1), slot, [lat.cuda()], c.latent_pages)
+    codes, s = F.quant(_vals(lat))
+    c.lat[0][0], c.lat_s[0][0] = F.dequant(codes, s), s
+    return c
+
+
+def _attend_list(c, q, keys, ws):
+    """The attention of one row (q bf16 [32, 576]) over its list, in this order; checked against the oracle."""
+    cfg, n = lsa.LsaConfig(cli_factor=1), c.lens[0]
+    idx = _i32(np.concatenate([keys, np.full(2048 - len(keys), -1)])[None])
+    out = [torch.full((1, 32, 512), 9.0, dtype=torch.bfloat16, device="cuda")]
+    lse = [torch.full((1, 32), 9.0, device="cuda")]
+    w = lsa.workspace(cfg, lsa.OP_FP8_MLA, 1, 1, n) if ws else None
+    lsa.fp8_sparse_mla(cfg, None, _i32([n - 1]), [q[None].cuda()], c.latent_pages, c.block_table, idx, _i32([len(keys)]),
+                       n, out, lse, w)
+    assert lsa.device_error() == 0
+    want, wl, wt = F.attend(_vals(q), c.lat[0][0], keys, cfg.softmax_scale)
+    tol, ltol = _mla_tol(_vals(q), c.lat[0][0], c.lat_s[0][0], keys, wt, want, cfg.softmax_scale)
+    o, l = _vals(out[0])[0], lse[0][0].double().cpu().numpy()
+    assert (np.abs(l - wl) <= ltol).all()
+    assert (np.abs(o - want) <= tol).all()
+    return o
+
+
+@gpu
+@pytest.mark.parametrize("ws", [False, True])      # one split, or several
+@pytest.mark.parametrize("n,zero_at", [(2, 0), (2, 1), (90, 40), (700, 0), (700, 650)])
+@pytest.mark.parametrize("amp,logit", [(1000.0, -41000.0), (2000.0, -139.0), (1e30, -400.0)])
+def test_mla_a_row_of_zeros_above_rows_of_large_scale(ws, n, zero_at, amp, logit):
+    # the row of zeros has the whole weight and every other row's is zero in fp32, beside a scale of up to 2^91
+    rng = np.random.default_rng(n + zero_at)
+    lat = _bf16(amp * rng.uniform(0.9, 1.0, (n, 576)))
+    lat[zero_at] = 0
+    q = _bf16(np.full((32, 576), logit * 192 ** 0.5 / (576 * 0.95 * amp)))
+    c = _sequence(lat)
+    o = _attend_list(c, q, np.arange(n), ws)
+    assert (np.abs(o) <= 1e-20 * amp).all()
+
+
+@gpu
+@pytest.mark.parametrize("ws", [False, True])
+@pytest.mark.parametrize("top", [400.0 * 2.0 ** -126, 440.0 * 2.0 ** -125, 2.0 ** -60])
+def test_mla_rows_of_the_smallest_scales(ws, top):
+    # among many of their kind, and alone: one key's values come out exactly
+    rng = np.random.default_rng(5)
+    lat = _bf16(rng.uniform(-top, top, (300, 576)))
+    lat[:, 0] = top
+    c = _sequence(lat)
+    assert (c.lat_s[0][0] == (2.0 ** -68 if top == 2.0 ** -60 else 2.0 ** -126 if top < 448 * 2.0 ** -126 else 2.0 ** -125)).all()
+    q = _bf16(rng.standard_normal((32, 576)))
+    _attend_list(c, q, np.arange(300), ws)
+    for k in (0, 131, 299):
+        o = _attend_list(c, q, np.array([k]), ws)
+        normal = np.abs(c.lat[0][0][k, :512]) >= 2.0 ** -126
+        assert normal.sum() > 500 and (o[:, normal] == c.lat[0][0][k, :512][normal]).all()
