@@ -73,7 +73,7 @@ constexpr int kMaxSplits = 32;
 constexpr uint32_t kTmemO = 128;                 // S: columns 0..127, O: 128..383
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kUnset = -1.0e9f;                // no frame yet
+constexpr float kUnset = -3.0e38f;               // no frame yet
 
 struct __align__(1024) Fp8MlaSmem {
   uint8_t k[2][kStageBytes];
@@ -642,7 +642,7 @@ __device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& s
     float L[kHG];
 #pragma unroll
     for (int j = 0; j < kHG; ++j) L[j] = f.m[j] = f.w[j] = 0.f;
-    float m_h = 0.f, d_h = kUnset, a_h = kUnset, a_top = kUnset;  // head h's frames (the same in every warp of the group)
+    float m_h = 0.f, d_h = kUnset, d_top = kUnset;  // head h's frames, m and A - m (the same in every warp of the group)
     bool framed = false, dead = false;
     for (int t = t0; t < t1; ++t, ++g) {
       const int b = g & 1;
@@ -689,19 +689,24 @@ __device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& s
           tl = fmaxf(tl, sm.tmax[w0 + w][h].x);
           ta = fmaxf(ta, sm.tmax[w0 + w][h].y);
         }
-        const float m_old = m_h, a_old = a_h;
+        const float m_old = m_h;
         if (tl > -INFINITY) m_h = framed ? fmaxf(m_old, tl + m_old) : tl + m_old;
-        if (ta > -INFINITY) {
-          // down by at most 2^60 from the item's highest: O, scaled up by as much, stays far from overflow;
-          // and to no less than 2^-124 of m: the weights' factor and O's are then powers of two in range
-          d_h = fmaxf(ceilf(fmaxf(ta + m_old, anew ? a_top - 60.f : a_old) - m_h), -124.f);
-          a_h = m_h + d_h;
-          a_top = fmaxf(a_top, a_h);
+        const float dm = m_h - m_old;
+        // A goes by its distance from m, before the move: where no key of the tile adds to O it stays, and
+        // the distance changes all the same. Down by at most 2^60 from the item's highest: O, scaled up by as
+        // much, stays far from overflow. No less than 2^-124 of m: the weights' factor and O's are then
+        // powers of two in range.
+        const float d_old = d_h;
+        const float to = ta > -INFINITY ? fmaxf(ta, anew ? d_top - 60.f : d_old) : d_old;
+        float of = 1.f;
+        if (to > kUnset) {
+          d_h = fmaxf(ceilf(to - dm), -124.f);
+          d_top = fmaxf(d_top - dm, d_h);
+          of = ex2(fminf(d_old - dm - d_h, 126.f));
         }
         framed = framed || __any_sync(0xffffffffu, tl > -INFINITY);
-        const float of = ex2(fminf(a_old - a_h, 126.f));
         __syncwarp();
-        frame[h] = make_float4(-m_h, pow2f(fminf(2.f - d_h, 126.f)), ex2(fminf(m_old - m_h, 126.f)), of);
+        frame[h] = make_float4(-m_h, pow2f(fminf(2.f - d_h, 126.f)), ex2(fminf(-dm, 126.f)), of);
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < kHG; ++j) {
@@ -759,7 +764,7 @@ __device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& s
     if (quarter == 0) {
       const float l = (sm.lsum[w0][h] + sm.lsum[w0 + 1][h]) + (sm.lsum[w0 + 2][h] + sm.lsum[w0 + 3][h]);
       const int f = nk & 3;
-      sm.fin[f][group * kHG + h] = make_float2(a_h == kUnset ? 0.f : pow2f(d_h - 2.f), l);
+      sm.fin[f][group * kHG + h] = make_float2(d_h == kUnset ? 0.f : pow2f(d_h - 2.f), l);
       sm.fin_m[f][group * kHG + h] = m_h;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.fin_full[f]);

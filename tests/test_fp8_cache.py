@@ -1189,3 +1189,40 @@ def test_mla_rows_of_the_smallest_scales(ws, top):
         o = _attend_list(c, q, np.array([k]), ws)
         normal = np.abs(c.lat[0][0][k, :512]) >= 2.0 ** -126
         assert normal.sum() > 500 and (o[:, normal] == c.lat[0][0][k, :512][normal]).all()
+
+
+@gpu
+@pytest.mark.parametrize("ws", [False, True])
+@pytest.mark.parametrize("loud,zeros,after,logit", [(128, 1, 0, -50.0), (128, 128, 128, -50.0), (256, 200, 300, -45.0),
+                                                    (2048 - 128, 128, 0, -60.0), (128 * 15, 127, 1, -80.0)])
+def test_mla_tiles_of_zero_rows_move_the_sums_and_the_output_alike(ws, loud, zeros, after, logit):
+    # the maximum rises by far more than 2^60 in a tile whose rows are all zeros: what was summed so far falls with it
+    rng = np.random.default_rng(loud)
+    n = loud + zeros + after
+    lat = _bf16(rng.uniform(0.5, 1.0, (n, 576)))
+    lat[loud:loud + zeros] = 0
+    q = _bf16(np.full((32, 576), logit * 192 ** 0.5 / (576 * 0.75)))
+    c = _sequence(lat)
+    o = _attend_list(c, q, np.arange(n), ws)
+    assert (np.abs(o) <= 1e-14).all()
+
+
+@gpu
+def test_mla_a_new_frame_on_a_tile_of_zero_rows():
+    # every 16 tiles the frame is set anew, here (the 17th) from rows of zeros alone, 2^23 above what came before
+    rng = np.random.default_rng(7)
+    n = 18 * 128
+    lat = _bf16(rng.uniform(0.5, 1.0, (n, 576)))
+    lat[16 * 128:17 * 128] = 0
+    q = _bf16(np.full((32, 576), -16.0 * 192 ** 0.5 / (576 * 0.75)))
+    c = _sequence(lat)
+    cfg = lsa.LsaConfig(cli_factor=1)
+    out, lse = [torch.empty(1, 32, 512, dtype=torch.bfloat16, device="cuda")], [torch.empty(1, 32, device="cuda")]
+    lsa.fp8_sparse_mla(cfg, None, _i32([n - 1]), [q[None].cuda()], c.latent_pages, c.block_table, None, None, n, out, lse,
+                       None)
+    assert lsa.device_error() == 0
+    want, wl, wt = F.attend(_vals(q), c.lat[0][0], range(n), cfg.softmax_scale)
+    assert want.max() < 1e-4
+    tol, ltol = _mla_tol(_vals(q), c.lat[0][0], c.lat_s[0][0], range(n), wt, want, cfg.softmax_scale)
+    assert (np.abs(lse[0][0].double().cpu().numpy() - wl) <= ltol).all()
+    assert (np.abs(_vals(out[0])[0] - want) <= tol).all()
