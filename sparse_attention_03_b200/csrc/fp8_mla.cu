@@ -585,10 +585,13 @@ __device__ __forceinline__ void mma_role(const Fp8MlaArgs& a, const Split& sp, F
 // nothing to O. The product of a large scale and a low frame's factor would
 // overflow beside a p of zero, so a scale above 1 goes to p and one below to the
 // factor: u is exact wherever it counts, and infinite or NaN only where p is (or
-// where u is above 128 and the frame is raised).
+// where u is above 128 and the frame is raised). ROUNDED: each logit is rounded
+// before m is taken from it, as m was. Unrounded it can lie half a step of fp32 above
+// m, which is whole binades where logits are in the thousands and beyond.
 struct Frames {
   float m[kHG], w[kHG];  // -m, 2^(2 - A + m)
 };
+template <bool ROUNDED>
 __device__ __forceinline__ void weights(uint32_t s_addr, const Frames& f, bool valid, float sq, float su,
                                         float (&p)[kHG], float (&u)[kHG], float& top_p, float& top_u) {
   tmem_ld16_x2(s_addr, s_addr + kH, p, u);  // hi and lo
@@ -596,7 +599,8 @@ __device__ __forceinline__ void weights(uint32_t s_addr, const Frames& f, bool v
   const float s_up = fmaxf(su, 1.f), s_down = fminf(su, 1.f);
 #pragma unroll
   for (int h = 0; h < kHG; ++h) {
-    p[h] = ex2(fmaf(fmaf(u[h], 0.0625f, p[h]), sq, f.m[h]));
+    const float x = fmaf(u[h], 0.0625f, p[h]);
+    p[h] = ex2(ROUNDED ? __fadd_rn(__fmul_rn(x, sq), f.m[h]) : fmaf(x, sq, f.m[h]));
     u[h] = (p[h] * s_up) * (s_down * f.w[h]);
     top_p = fmaxf(top_p, p[h]);
     top_u = fmaxf(top_u, u[h]);
@@ -643,7 +647,7 @@ __device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& s
 #pragma unroll
     for (int j = 0; j < kHG; ++j) L[j] = f.m[j] = f.w[j] = 0.f;
     float m_h = 0.f, d_h = kUnset, d_top = kUnset;  // head h's frames, m and A - m (the same in every warp of the group)
-    bool framed = false, dead = false;
+    bool framed = false, dead = false, huge = false;
     for (int t = t0; t < t1; ++t, ++g) {
       const int b = g & 1;
       // The tile is here (this thread reads its scale), so the products of tile g - 2
@@ -663,22 +667,23 @@ __device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& s
       const float su = silent ? 0.f : s, sq = s * qf;
       const bool anew = (t - t0) % kFrameTiles == 0;
       float p[kHG], u[kHG], top_p = 0.f, top_u = 0.f;
-      bool force = anew || !framed || !ok, moved = false;
+      bool force = anew || !framed || !ok, moved = false, again = false;
       while (true) {
-        if (!force) weights(s_addr, f, valid, sq, su, p, u, top_p, top_u);
+        if (!force) {
+          if (huge) weights<true>(s_addr, f, valid, sq, su, p, u, top_p, top_u);
+          else weights<false>(s_addr, f, valid, sq, su, p, u, top_p, top_u);
+        }
         if (moved || !softmax_any(group, force || top_u > 128.f || top_p > 0x1p60f)) break;
-        force = false;
-        moved = true;
         // Set the frames from this tile's maxima (the group's four warps, the same values).
         __syncwarp();
         tmem_ld16_x2(s_addr, s_addr + kH, p, u);
-#pragma unroll
-        for (int j = 0; j < kHG; ++j) {
-          p[j] = valid ? fmaf(fmaf(u[j], 0.0625f, p[j]), sq, f.m[j]) : -INFINITY;
-        }
         const float e = (float)((int)(tail.x >> 23) - 127);
 #pragma unroll
-        for (int j = 0; j < kHG; ++j) u[j] = silent ? -INFINITY : p[j] + e;
+        for (int j = 0; j < kHG; ++j) {
+          const float x = __fmul_rn(fmaf(u[j], 0.0625f, p[j]), sq);
+          p[j] = valid ? x : -INFINITY;
+          u[j] = silent ? -INFINITY : (huge ? __fadd_rn(x, f.m[j]) : x) + e;
+        }
         const float tl_w = fold16<true>(p, lane), ta_w = fold16<true>(u, lane);
         sm.tmax[warp][h] = make_float2(tl_w, ta_w);
         dead = softmax_any(group, !ok || *abort_flag);
@@ -689,18 +694,23 @@ __device__ __forceinline__ void softmax_role(const Fp8MlaArgs& a, const Split& s
           tl = fmaxf(tl, sm.tmax[w0 + w][h].x);
           ta = fmaxf(ta, sm.tmax[w0 + w][h].y);
         }
-        const float m_old = m_h;
-        if (tl > -INFINITY) m_h = framed ? fmaxf(m_old, tl + m_old) : tl + m_old;
+        const float m_old = m_h, d_old = d_h;
+        if (tl > -INFINITY) m_h = framed ? fmaxf(m_old, tl) : tl;
         const float dm = m_h - m_old;
-        // A goes by its distance from m, before the move: where no key of the tile adds to O it stays, and
-        // the distance changes all the same. Down by at most 2^60 from the item's highest: O, scaled up by as
-        // much, stays far from overflow. No less than 2^-124 of m: the weights' factor and O's are then
-        // powers of two in range.
-        const float d_old = d_h;
-        const float to = ta > -INFINITY ? fmaxf(ta, anew ? d_top - 60.f : d_old) : d_old;
+        // Logits of whose fp32 steps an exponent would be lost: m first, and A by what lies beside it.
+        huge = huge || __any_sync(0xffffffffu, fabsf(m_h) > 1024.f);
+        force = huge && !again && __any_sync(0xffffffffu, fabsf(dm) > 0.f);
+        again = force;
+        moved = !force;
+        // A goes by its distance from m: where no key of the tile adds to O it stays, and the distance changes
+        // all the same. Down by at most 2^60 from the item's highest: O, scaled up by as much, stays far from
+        // overflow. No less than 2^-124 of m: the weights' factor and O's are then powers of two in range.
+        const bool loud = ta > -INFINITY && !force;
+        float to = d_old == kUnset ? kUnset : (loud && anew ? d_top - 60.f : d_old) - dm;
+        if (loud) to = fmaxf(to, huge ? ta : ta - m_h);
         float of = 1.f;
         if (to > kUnset) {
-          d_h = fmaxf(ceilf(to - dm), -124.f);
+          d_h = fmaxf(ceilf(to), -124.f);
           d_top = fmaxf(d_top - dm, d_h);
           of = ex2(fminf(d_old - dm - d_h, 126.f));
         }

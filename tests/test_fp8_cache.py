@@ -1226,3 +1226,26 @@ def test_mla_a_new_frame_on_a_tile_of_zero_rows():
     tol, ltol = _mla_tol(_vals(q), c.lat[0][0], c.lat_s[0][0], range(n), wt, want, cfg.softmax_scale)
     assert (np.abs(lse[0][0].double().cpu().numpy() - wl) <= ltol).all()
     assert (np.abs(_vals(out[0])[0] - want) <= tol).all()
+
+
+@gpu
+@pytest.mark.parametrize("ws", [False, True])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("amp", [3e3, 1e5, 1e9, 1e15])
+def test_mla_logits_whose_fp32_steps_are_whole_binades(ws, sign, amp):
+    # logits from 2^24 to 2^100: an exponent added to one is lost in it. One key's values stay exact, and among many
+    # the best one's stand alone (its lead is far above the logits' rounding)
+    rng = np.random.default_rng(77)
+    lat = _bf16(rng.standard_normal((300, 576)) * 3 + sign * 2.0) * amp
+    lat = lat.bfloat16()
+    q = (_bf16(rng.uniform(0.5, 1.5, (32, 576))) * amp).bfloat16()
+    c = _sequence(lat)
+    v = c.lat[0][0][:, :512]
+    for k in (0, 131, 299):
+        assert (_attend_list(c, q, np.array([k]), ws) == v[k]).all()
+    x = lsa.LsaConfig().softmax_scale * (_vals(q) @ c.lat[0][0].T)
+    for keys in (np.arange(300), np.argsort(x[5])):
+        o = _attend_list(c, q, keys, ws)
+        lead = np.sort(x, axis=1)
+        clear = lead[:, -1] - lead[:, -2] > 2.0 ** -10 * np.abs(lead).max()
+        assert clear.any() and (o[clear] == v[x.argmax(1)][clear]).all()
