@@ -295,7 +295,7 @@ __device__ __forceinline__ bool write_out(const Fp8MlaArgs& a, const Split& sp, 
     if (!one) part_ml[base * kH + lane] = make_float2(m, fin.y);
     else if (a.lse[z]) a.lse[z][(int64_t)r * kH + lane] = fin.y == 0.f ? -INFINITY : (m + log2f(fin.y)) * kLn2;
   }
-  const float mine = !one ? fin.x : fin.y == 0.f ? 0.f : fin.x / fin.y;
+  const float mine = fin.y == 0.f ? 0.f : fin.x / fin.y;  // a split's share too: its sum alone could leave fp32's range
 #pragma unroll 1
   for (int c = 0; c < 8; ++c) {  // 128 dims, 16 heads at a time (the gather's registers hold a tile)
     const int h0 = (c & 1) * 16;
@@ -850,7 +850,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 __global__ void __launch_bounds__(128)
     fp8_mla_merge_kernel(const __grid_constant__ Fp8MlaArgs a, int n_split, const float* part_o, const float2* part_ml, int row0) {
   __shared__ float wgt[kMaxSplits];
-  __shared__ float inv_l;
   pdl_wait();
   const int h = blockIdx.x, r = row0 + blockIdx.y, z = blockIdx.z, tid = threadIdx.x;
   const int seq = a.rows.seq_of_row ? a.rows.seq_of_row[r] : r;
@@ -868,9 +867,8 @@ __global__ void __launch_bounds__(128)
     float L = live ? wv * ml.y : 0.f;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-    if (there) wgt[tid] = live ? wv : -1.f;
+    if (there) wgt[tid] = live ? wv * ml.y / L : -1.f;  // of outputs that are divided by their own sums
     if (tid == 0) {
-      inv_l = L == 0.f ? 0.f : 1.f / L;
       if (a.lse[z]) a.lse[z][(int64_t)r * kH + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
     }
   }
@@ -887,8 +885,7 @@ __global__ void __launch_bounds__(128)
     acc.z = fmaf(wv, x.z, acc.z);
     acc.w = fmaf(wv, x.w, acc.w);
   }
-  const float il = inv_l;
-  const uint2 pk = make_uint2(bf16x2_rn(acc.x * il, acc.y * il), bf16x2_rn(acc.z * il, acc.w * il));
+  const uint2 pk = make_uint2(bf16x2_rn(acc.x, acc.y), bf16x2_rn(acc.z, acc.w));
   *reinterpret_cast<uint2*>(a.out[z] + ((int64_t)r * kH + h) * kDV + tid * 4) = pk;
 }
 

@@ -1249,3 +1249,17 @@ def test_mla_logits_whose_fp32_steps_are_whole_binades(ws, sign, amp):
         lead = np.sort(x, axis=1)
         clear = lead[:, -1] - lead[:, -2] > 2.0 ** -10 * np.abs(lead).max()
         assert clear.any() and (o[clear] == v[x.argmax(1)][clear]).all()
+
+
+@gpu
+@pytest.mark.parametrize("ws", [False, True])
+def test_mla_partials_of_the_largest_values_stay_finite(ws):
+    # values near bf16's largest: the sum over a split's keys is infinite in fp32 unless it is divided by its weights
+    rng = np.random.default_rng(9)
+    lat = _bf16(rng.uniform(2e38, 3e38, (700, 576)))
+    q = _bf16(rng.standard_normal((32, 576)) * 1e-38)
+    c = _sequence(lat)
+    assert (c.lat_s[0][0] == 2.0 ** 120).mean() > 0.9 and c.lat[0][0].max() < 2.0 ** 128
+    _attend_list(c, q, np.arange(700), ws)
+    o = _attend_list(c, q, np.array([5]), ws)
+    assert (o == c.lat[0][0][5, :512]).all()
