@@ -916,12 +916,14 @@ cudaError_t launch_rows(const Fp8IndexArgs& a, const CUtensorMap& map, cudaStrea
   return e;
 }
 
-cudaError_t launch_blocks(const Fp8IndexArgs& a, const CUtensorMap& map, cudaStream_t st) {
+cudaError_t launch_blocks(Fp8IndexArgs a, const CUtensorMap& map, cudaStream_t st) {
   static bool done[64];
   const int n_rows = a.rows.n_rows;
   uint8_t* codes = static_cast<uint8_t*>(a.ws);
   float* wq = reinterpret_cast<float*>(codes + (size_t)n_rows * kHi * kDi);
   int* block_cost = reinterpret_cast<int*>(wq + (size_t)n_rows * kHi);
+  // the histograms count what a row sees, which its position alone does not say
+  if (a.hist && !a.top_pos) a.top_pos = block_cost + (n_rows + kRows - 1) / kRows;
   CUtensorMap map_q;
   if (!query_map(&map_q, codes, (int64_t)n_rows * kHi)) return cudaErrorInvalidValue;
   cudaError_t e = launch_pdl(fp8_index_query_kernel, dim3((unsigned)(((int64_t)n_rows * kHi * 16 + 255) / 256)), dim3(256), 0,
@@ -944,7 +946,7 @@ cudaError_t launch_blocks(const Fp8IndexArgs& a, const CUtensorMap& map, cudaStr
   TopkArgs t;
   t.scores = a.scores;
   t.ld = a.ld;
-  t.pos = a.rows.pos;
+  t.pos = a.top_pos;
   t.n_rows = n_rows;
   t.max_len = a.rows.max_len;
   t.topk = a.topk;
@@ -959,9 +961,9 @@ cudaError_t launch_blocks(const Fp8IndexArgs& a, const CUtensorMap& map, cudaStr
 
 }  // namespace
 
-// the block form's quantised queries and tile counts; asked for whichever form the rows take
+// the block form's quantised queries, costs and last visible keys; asked for whichever form the rows take
 size_t fp8_index_ws_bytes(int n_rows) {
-  return (size_t)n_rows * kHi * (kDi + sizeof(float)) + (size_t)((n_rows + kRows - 1) / kRows) * sizeof(int);
+  return (size_t)n_rows * (kHi * (kDi + sizeof(float)) + sizeof(int)) + (size_t)((n_rows + kRows - 1) / kRows) * sizeof(int);
 }
 
 bool fp8_index_streams(int n_rows, int n_seq, int64_t max_len) { return !use_blocks(n_rows, n_seq, max_len); }

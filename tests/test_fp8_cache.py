@@ -1263,3 +1263,32 @@ def test_mla_partials_of_the_largest_values_stay_finite(ws):
     _attend_list(c, q, np.arange(700), ws)
     o = _attend_list(c, q, np.array([5]), ws)
     assert (o == c.lat[0][0][5, :512]).all()
+
+
+@gpu
+@pytest.mark.parametrize("bound", [400, 60000])     # the kernel's two forms
+def test_scores_histogram_of_rows_without_a_sequence_or_past_their_table(bound):
+    # positions that look real beside no sequence count nothing; one past the table counts what the row sees
+    cfg = lsa.LsaConfig(**TINY)
+    c = Caches([300, 150], 3)
+    rows = [(s, p) for s, n in enumerate(c.lens) for p in range(n - 30, n)]
+    rows[5:5] = [(-1, 250), (2, 250), (-9, 299), (0, 350), (-1, 2 ** 31 - 1), (0, -4)]
+    rows += [(-1, 120), (-1, 299)]
+    n = len(rows)
+    rng = np.random.default_rng(4)
+    q = _bf16(rng.standard_normal((n, 32, 128))).cuda()
+    w = torch.from_numpy(rng.standard_normal((n, 32)).astype(np.float32)).cuda()
+    scores = torch.full((n, bound), 7.0, device="cuda")
+    h = lsa.topk_hist_buffer(n)
+    ws = lsa.workspace(cfg, lsa.OP_FP8_INDEX, n, 2, bound)
+    for _ in range(2):
+        h.fill_(3)
+        lsa.fp8_index_scores(cfg, _i32([r[0] for r in rows]), _i32([r[1] for r in rows]), q, w, c.key_pages, c.block_table,
+                             bound, scores, ws, topk_hist=h)
+        assert lsa.device_error() == lsa.DEVERR_SEQ | lsa.DEVERR_POS
+    room = c.table.shape[1] * 64
+    assert room == 320
+    seen = [(-1 if s not in (0, 1) or p < 0 else s, min(p, room - 1)) for s, p in rows]
+    for r, (s, p) in enumerate(seen):
+        assert (scores[r, p + 1 if s >= 0 else 0:] == 7.0).all()
+    _check_hist(seen, scores, h, cfg)
