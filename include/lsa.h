@@ -515,7 +515,8 @@ LSA_API lsa_status lsa_forward(const lsa_config* cfg, int32_t mode, int32_t n_ro
  * totals[0] > n_rows sets LSA_DEVERR_COUNT (the rows beyond are not written);
  * totals[1] > n_free, or a negative or too large page number met on the way,
  * sets LSA_DEVERR_PAGE (entry and slots -1). A request with a negative length
- * or with cached + fresh > max_pages * 64 sets LSA_DEVERR_POS and gets nothing.
+ * or with cached + fresh > min(max_pages, 2^25 - 1) * 64 sets LSA_DEVERR_POS and
+ * gets nothing.
  * Running it again with the same inputs writes the same outputs.
  */
 #define LSA_PLAN_MAX_SEQ 16384

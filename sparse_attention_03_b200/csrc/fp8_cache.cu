@@ -64,7 +64,8 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PagePlanArgs a)
   uint32_t* pages = sh + a.n_seq + 1;   // [n_seq + 1]
   pdl_wait();
   const bool report = blockIdx.x == 0;
-  const int64_t room = (int64_t)a.max_pages * kPage;
+  // A table may be wider than the largest pool: what is beyond has no page, and positions stay in 32 bits.
+  const int64_t room = min64(a.max_pages, kMaxPages) * kPage;
   for (int s = threadIdx.x; s < a.n_seq; s += kPlanThreads) {
     const int64_t c = a.cached[s], f = a.fresh[s];
     uint32_t nr = 0, np = 0;

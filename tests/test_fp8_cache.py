@@ -1292,3 +1292,24 @@ def test_scores_histogram_of_rows_without_a_sequence_or_past_their_table(bound):
     for r, (s, p) in enumerate(seen):
         assert (scores[r, p + 1 if s >= 0 else 0:] == 7.0).all()
     _check_hist(seen, scores, h, cfg)
+
+
+@gpu
+def test_page_plan_at_the_largest_lengths():
+    # a table wider than any pool: lengths go up to 2^31 - 64, and what is longer is refused like any other
+    width, most = 2 ** 25 + 1, 2 ** 31 - 64
+    bt = torch.full((3, width), -1, dtype=torch.int32, device="cuda")
+    bt[0, 2 ** 25 - 2], bt[2, 0] = 7, 3
+    cached, fresh = [most - 2, 2 ** 31 - 10, 3], [2, 5, 62]
+    free = [11, 12]
+    seq, pos, slot, totals = (_i32([55] * k) for k in (66, 66, 66, 2))
+    lsa.page_plan(_i32(cached), _i32(fresh), _i32(free), bt, seq, pos, slot, totals)
+    assert lsa.device_error() == lsa.DEVERR_POS
+    assert totals.tolist() == [64, 1]
+    assert seq.tolist() == [0] * 2 + [2] * 62 + [-1] * 2
+    assert pos.tolist() == [most - 2, most - 1] + list(range(3, 65)) + [-1] * 2
+    assert slot.tolist() == [7 * 64 + 62, 7 * 64 + 63] + [3 * 64 + i for i in range(3, 64)] + [11 * 64, -1, -1]
+    assert int(bt[2, 1]) == 11 and int((bt != -1).sum()) == 3
+    # the request that is one token too long for 32-bit columns
+    lsa.page_plan(_i32([most]), _i32([1]), _i32(free), bt[:1], seq, pos, slot, totals)
+    assert lsa.device_error() == lsa.DEVERR_POS and totals.tolist() == [0, 0] and int((bt != -1).sum()) == 3
