@@ -1313,3 +1313,14 @@ def test_page_plan_at_the_largest_lengths():
     # the request that is one token too long for 32-bit columns
     lsa.page_plan(_i32([most]), _i32([1]), _i32(free), bt[:1], seq, pos, slot, totals)
     assert lsa.device_error() == lsa.DEVERR_POS and totals.tolist() == [0, 0] and int((bt != -1).sum()) == 3
+
+
+def test_barrier_operations_order_plain_accesses():
+    # published and consumed shared data are plain accesses: every arrival and wait is a barrier for the compiler too
+    import re
+    from pathlib import Path
+
+    src = (Path(lsa.__file__).parent / "csrc" / "tc.cuh").read_text()
+    for name in ("mbar_expect_tx", "mbar_arrive", "mbar_try_wait", "mbar_test"):
+        body = re.search(rf"\b{name}\(uint64_t\* bar.*?\n}}\n", src, re.S).group(0)
+        assert '"memory"' in body, name
