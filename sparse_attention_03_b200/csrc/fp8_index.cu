@@ -853,18 +853,6 @@ bool use_blocks(int64_t n_rows, int64_t n_seq, int64_t max_len) {
   return 20 * 8000 + (70 * runs + 26 * groups) * tiles < 35 * n_rows * tiles;
 }
 
-int sm_count() {
-  static int cache[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
-  if (cache[dev] == 0) {
-    int s = 148;
-    if (cudaDeviceGetAttribute(&s, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || s < 1) s = 148;
-    cache[dev] = s;
-  }
-  return cache[dev];
-}
-
 template <typename K>
 cudaError_t set_smem(K kernel, int bytes, bool (&done)[64]) {
   int dev = 0;

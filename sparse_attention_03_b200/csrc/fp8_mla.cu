@@ -889,18 +889,6 @@ __global__ void __launch_bounds__(128)
   *reinterpret_cast<uint2*>(a.out[z] + ((int64_t)r * kH + h) * kDV + tid * 4) = pk;
 }
 
-int sm_count() {
-  static int cache[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
-  if (cache[dev] == 0) {
-    int s = 148;
-    if (cudaDeviceGetAttribute(&s, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || s < 1) s = 148;
-    cache[dev] = s;
-  }
-  return cache[dev];
-}
-
 // Splits of each row's list: the count with the shortest longest CTA, an item
 // costing its tiles plus about two tiles' time of its own (query, output) and
 // the join of the splits about one more. Measured with 1, 2, 4, 8 and 16 splits

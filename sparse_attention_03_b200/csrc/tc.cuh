@@ -137,7 +137,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-
 // A 32-column load in two halves: its request, and the wait that makes the
 // registers valid (they pass through it, so that no use moves before it). What is
 // computed in between hides the load.
@@ -167,29 +166,6 @@ __device__ __forceinline__ void tmem_ld16_x2(uint32_t ta, uint32_t tb, float (&a
   asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    a[i] = __uint_as_float(r[0][i]);
-    b[i] = __uint_as_float(r[1][i]);
-  }
-}
-
-// Two 32-column loads issued back to back and one wait.
-__device__ __forceinline__ void tmem_ld32_x2(uint32_t ta, uint32_t tb, float (&a)[32], float (&b)[32]) {
-  uint32_t r[2][32];
-#pragma unroll
-  for (int q = 0; q < 2; ++q)
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-        : "=r"(r[q][0]), "=r"(r[q][1]), "=r"(r[q][2]), "=r"(r[q][3]), "=r"(r[q][4]), "=r"(r[q][5]),
-          "=r"(r[q][6]), "=r"(r[q][7]), "=r"(r[q][8]), "=r"(r[q][9]), "=r"(r[q][10]), "=r"(r[q][11]),
-          "=r"(r[q][12]), "=r"(r[q][13]), "=r"(r[q][14]), "=r"(r[q][15]), "=r"(r[q][16]), "=r"(r[q][17]),
-          "=r"(r[q][18]), "=r"(r[q][19]), "=r"(r[q][20]), "=r"(r[q][21]), "=r"(r[q][22]), "=r"(r[q][23]),
-          "=r"(r[q][24]), "=r"(r[q][25]), "=r"(r[q][26]), "=r"(r[q][27]), "=r"(r[q][28]), "=r"(r[q][29]),
-          "=r"(r[q][30]), "=r"(r[q][31])
-        : "r"(q == 0 ? ta : tb));
-  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) {
     a[i] = __uint_as_float(r[0][i]);
     b[i] = __uint_as_float(r[1][i]);
   }
@@ -258,17 +234,6 @@ __host__ __device__ constexpr uint32_t f8_idesc(uint32_t n, bool mn) {
 __device__ __forceinline__ uint64_t sw64_mn_desc(uint32_t saddr) {
   return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(512 >> 4) << 16) | ((uint64_t)(512 >> 4) << 32) |
          ((uint64_t)1 << 46) | ((uint64_t)4 << 61);
-}
-
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
-      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]),
-      "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]),
-      "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]),
-      "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31]));
-  asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
 }
 
 // Two 16-column stores and one wait.
