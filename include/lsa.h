@@ -474,6 +474,9 @@ LSA_API lsa_status lsa_forward(const lsa_config* cfg, int32_t mode, int32_t n_ro
  * nearest-even e4m3. x_i / s is exact, so the codes are a function of the bits
  * of x alone. A vector holding an infinity or NaN gets scale NaN and zero
  * codes: it stands for NaN throughout. The cached vector stands for scale * code.
+ * A scale is never 0: a slot whose scale is (a zeroed pool's, before its append)
+ * holds no key, and where a row lists or sees it all the same the attention skips
+ * it and the indexer's score of it is 0.
  *
  * Latent pages: uint8 [n_pages, 64, LSA_FP8_LATENT_ROW]: a token's 576 codes,
  *   its fp32 scale at byte 576, a uint32 at byte 580 (1 when every code is zero,

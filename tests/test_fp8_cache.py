@@ -1324,3 +1324,152 @@ def test_barrier_operations_order_plain_accesses():
     for name in ("mbar_expect_tx", "mbar_arrive", "mbar_try_wait", "mbar_test"):
         body = re.search(rf"\b{name}\(uint64_t\* bar.*?\n}}\n", src, re.S).group(0)
         assert '"memory"' in body, name
+
+
+# ------------------------------------------------------------------ GPU: layers at once and replayed, every row checked
+
+
+class _Layer:
+    """A layer call over sequences of its own, its outputs poisoned before each run."""
+
+    def __init__(self, seed, n, max_len, lens):
+        self.cfg = lsa.LsaConfig(index_topk=96, index_init_tokens=4, index_local_tokens=16)
+        self.c = Caches(lens, seed, cli=2)
+        self.rng = np.random.default_rng(seed + 1)
+        self.n, self.max_len = n, max_len
+        self.q_idx, self.w, self.q, self.out, self.lse = _layer_inputs(self.rng, n)
+        self.seq, self.pos = (torch.empty(n, dtype=torch.int32, device="cuda") for _ in range(2))
+        self.idx = torch.empty(n, 96, dtype=torch.int32, device="cuda")
+        self.cnt = torch.empty(n, dtype=torch.int32, device="cuda")
+        self.ws = lsa.workspace(self.cfg, lsa.OP_FP8_FORWARD, n, len(lens), max_len)
+
+    def new_rows(self):
+        s = np.sort(self.rng.integers(-1, len(self.c.lens), self.n))[::-1].copy()
+        self.seq.copy_(_i32(s))
+        self.pos.copy_(_i32([self.rng.integers(0, self.c.lens[k]) if k >= 0 else -1 for k in s]))
+        for x in (self.q_idx, *self.q):
+            x.copy_(_bf16(self.rng.standard_normal(tuple(x.shape))))
+
+    def poison(self):
+        for t in (*self.out, *self.lse):
+            t.fill_(9.0)
+        self.idx.fill_(-9)
+        self.cnt.fill_(-9)
+        self.ws.fill_(0xFF)
+
+    def run(self):
+        lsa.fp8_forward(self.cfg, self.seq, self.pos, self.max_len, self.q_idx, self.w, self.c.key_pages, self.q,
+                        self.c.latent_pages, self.c.block_table, self.out, self.lse, self.ws, idx_out=self.idx,
+                        count_out=self.cnt)
+
+    def check(self):
+        ocfg = R.LsaConfig(index_topk=96, index_init_tokens=4, index_local_tokens=16)
+        seq, pos, idx, cnt = (t.cpu().numpy() for t in (self.seq, self.pos, self.idx, self.cnt))
+        qi, w = _vals(self.q_idx), self.w.double().cpu().numpy()
+        q, out, lse = ([_vals(t) for t in ts] for ts in (self.q, self.out, self.lse))
+        for r, (s, p) in enumerate(zip(seq, pos)):
+            if s < 0:
+                assert cnt[r] == 0 and (idx[r] == -1).all()
+                assert all((o[r] == 9.0).all() for o in out) and all((l[r] == 9.0).all() for l in lse)
+                continue
+            sel = idx[r, :cnt[r]]
+            assert len(set(sel.tolist())) == cnt[r] == min(p + 1, 96) and sel.min() >= 0 and sel.max() <= p
+            want_idx, gap = R.select_topk(F.score_row(qi[r], w[r], self.c.keys[s], p, ocfg), p, ocfg)
+            if p + 1 > 96 and gap is not None and gap > 1e-4:
+                np.testing.assert_array_equal(np.sort(sel), np.sort(want_idx))
+            for z in range(2):
+                o, l, wt = F.attend(q[z][r], self.c.lat[z][s], sel, self.cfg.softmax_scale)
+                tol, ltol = _mla_tol(q[z][r], self.c.lat[z][s], self.c.lat_s[z][s], sel, wt, o, self.cfg.softmax_scale)
+                assert (np.abs(lse[z][r] - l) <= ltol).all()
+                assert (np.abs(out[z][r] - o) <= tol).all()
+
+
+@gpu
+def test_layers_at_once_write_every_row():
+    layers = [_Layer(71, 66, 60000, [300, 900]), _Layer(74, 3, 900, [900, 130]), _Layer(77, 40, 400, [400, 17, 250])]
+    streams = [torch.cuda.Stream() for _ in layers]
+    for _ in range(3):
+        for a in layers:
+            a.new_rows()
+            a.poison()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for a, st in zip(layers, streams):
+                with torch.cuda.stream(st):
+                    a.poison()
+                    a.run()
+        torch.cuda.synchronize()
+        assert lsa.device_error() == 0
+        for a in layers:
+            a.check()
+
+
+@gpu
+@pytest.mark.parametrize("max_len", [300, 60000])     # the indexer's two forms
+def test_replayed_layers_write_every_row(max_len):
+    # two captured layers, replayed in turn with new rows and queries in place: nothing stands from an earlier run
+    layers = [_Layer(81, 66, max_len, [300, 260]), _Layer(84, 5, max_len, [300, 90])]
+    graphs = []
+    for a in layers:
+        a.new_rows()
+        a.run()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            a.run()
+        graphs.append(g)
+    for _ in range(3):
+        for a, g in zip(layers, graphs):
+            a.new_rows()
+            a.poison()
+            g.replay()
+        torch.cuda.synchronize()
+        assert lsa.device_error() == 0
+        for a in layers:
+            a.check()
+    del graphs, g
+
+
+# ------------------------------------------------------------------ GPU: rows that one key dominates, slots never filled
+
+
+@gpu
+@pytest.mark.parametrize("ws", [False, True])
+@pytest.mark.parametrize("weight", [0.9, 0.99, 0.999])
+@pytest.mark.parametrize("along", [20.0, 2.0])        # the sink's scale: half of the other rows', or eight times it
+def test_mla_rows_that_a_sink_dominates(ws, weight, along):
+    # the other keys' weights lie 2^-14 to 2^-21 below the sink's, where the steps of a weight's code (2^-16 of the
+    # largest weight * scale and coarser) are of their own size: the error stays within those steps' sum
+    rng = np.random.default_rng(int(weight * 1000))
+    n = 2048
+    u = rng.standard_normal(576)
+    u /= np.linalg.norm(u)
+    q = _bf16(along * u + 0.2 * rng.standard_normal((32, 576)))
+    x = rng.standard_normal((n, 576))
+    x[1:] -= np.outer(x[1:] @ u, u)                    # the others have no part in the heads' common direction
+    x[0] = u * (np.log(weight / (1 - weight)) + np.log(n - 1)) * 192 ** 0.5 / along
+    c = _sequence(_bf16(x))
+    o = _attend_list(c, q, np.arange(n), ws)
+    _, _, wt = F.attend(_vals(q), c.lat[0][0], range(n), lsa.LsaConfig().softmax_scale)
+    # (the case is what it says: heads differ by their own parts' products with the sink)
+    assert abs(np.median(np.log(wt[:, 0] / (1 - wt[:, 0]))) - np.log(weight / (1 - weight))) < 1
+    assert np.isfinite(o).all()
+
+
+@gpu
+def test_slots_that_were_never_filled_hold_no_key():
+    # a scale of 0 stands in no appended row: the attention skips it, the indexer's score of it is 0
+    c = Caches([200], 91, cli=1)
+    slots = c.slots(0, 200)
+    for k in (3, 64, 130):
+        c.latent_pages[0].view(-1, F.LAT_ROW)[slots[k]] = 0
+        c.key_pages.view(torch.float32)[slots[k] // 64, 2048 + slots[k] % 64] = 0
+    cfg = lsa.LsaConfig(index_topk=64, index_init_tokens=1, index_local_tokens=2, cli_factor=1)
+    lists = [[3, 64, 130], [2, 3, 4, 64, 199], list(range(60, 120))]
+    _mla_case(c, [(0, 199)] * 3, lists, cfg, keep=lambda s, k: k not in (3, 64, 130))
+    q = _bf16(np.random.default_rng(1).standard_normal((1, 32, 128))).cuda()
+    scores, w = torch.full((1, 200), 7.0, device="cuda"), torch.ones(1, 32, device="cuda")
+    lsa.fp8_index_scores(cfg, None, _i32([199]), q, w, c.key_pages, c.block_table, 200, scores,
+                         lsa.workspace(cfg, lsa.OP_FP8_INDEX, 1, 1, 200))
+    assert lsa.device_error() == 0
+    assert scores[0, [3, 64, 130]].tolist() == [0.0] * 3 and bool((scores[0] != 7.0).all())
