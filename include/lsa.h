@@ -496,7 +496,8 @@ LSA_API lsa_status lsa_forward(const lsa_config* cfg, int32_t mode, int32_t n_ro
  * written. Another number outside [0, n_seq) sets LSA_DEVERR_SEQ (no scores, or
  * zero output with lse -inf); a position < 0, or past max_len or max_pages * 64,
  * sets LSA_DEVERR_POS and is clamped. A page outside the pool sets
- * LSA_DEVERR_PAGE; its keys are never read (score -inf; skipped by the attention).
+ * LSA_DEVERR_PAGE; its keys are never read (score -inf, where the column is not
+ * forced; skipped by the attention).
  */
 #define LSA_PAGE_TOKENS 64
 #define LSA_FP8_LATENT_ROW 592
@@ -550,9 +551,12 @@ LSA_API lsa_status lsa_fp8_append(const lsa_config* cfg, int32_t n_rows, const i
  * cached keys as they stand (k8, sk):
  *   scores[r, j] = sum_h w[r,h] * max(0, sq[r,h] * sk[j] * (q8[r,h,:] . k8[j,:]))
  * for j <= pos[r]; forced columns +inf; other entries are not written. The
- * products of codes are exact and summed in fp32.
+ * products of codes are exact and summed in fp32, before sk: the largest element
+ * of a query times sum_h |w[r,h]| has to stay below 2^110.
  * q_idx bf16 [n_rows, 32, 128]; w fp32 [n_rows, 32]; scores fp32 [n_rows, ld],
- * ld >= max_len; every pos[r] < max_len. topk_hist: as lsa_index_scores.
+ * ld >= max_len; every pos[r] < max_len. topk_hist: as lsa_index_scores; all zeros
+ * for a row without a sequence, and of the keys it sees for one whose position is
+ * clamped (lsa_topk takes positions alone: give it -1 and the clamped one there).
  * Workspace: lsa_workspace_size(LSA_OP_FP8_INDEX) (the quantised queries).
  */
 LSA_API lsa_status lsa_fp8_index_scores(const lsa_config* cfg, int32_t n_rows, int32_t n_seq,
@@ -578,8 +582,10 @@ LSA_API lsa_status lsa_fp8_index_scores(const lsa_config* cfg, int32_t n_rows, i
  * [n_rows, 32, 512], lse fp32 [n_rows, 32]. The query enters to its last bit
  * (to 2^-22 of the row's largest element; a query with an
  * infinity or NaN gives NaN); the softmax weights times their
- * scales are rounded to 8 significant bits, as a bf16 weight is, and lost below
- * 2^-17 of the largest of them. Logits, sums and outputs accumulate in fp32.
+ * scales are rounded to 8 significant bits, as a bf16 weight is, and to steps of
+ * 2^-16 of the largest of them: what is below 2^-17 of it is lost (its weight still
+ * counts in the sum), as is a weight below 2^-126 of the row's largest. Logits, sums
+ * and outputs accumulate in fp32.
  * Workspace optional (split-K partials): lsa_workspace_size(LSA_OP_FP8_MLA).
  */
 LSA_API lsa_status lsa_fp8_sparse_mla(const lsa_config* cfg, int32_t n_sub, int32_t n_rows, int32_t n_seq,

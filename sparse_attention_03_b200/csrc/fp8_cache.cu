@@ -147,8 +147,11 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PagePlanArgs a)
 // bytes go round the lanes (288 chunks of a latent: nine full loads a lane, all in
 // flight; one row a warp leaves the third of three loads three quarters idle).
 // Largest magnitudes on the bit patterns, then a multiply and a conversion per
-// element. Bound by HBM: 16384 rows (2 sub-blocks and the key) 15.7 us, 4.0 TB/s;
-// one row a warp took 25. 64 rows: 4.0 us, a launch.
+// element. Bound by the latency of a warp's one chain, slot -> loads -> maxima ->
+// stores (top stall: long scoreboard; DRAM 31 %, ALU 55 %, issue 0.55): a warp loads
+// nothing under its own stores. 16384 rows (2 sub-blocks and the key, 63 MB, which
+// stay in L2 from call to call) 15.8 us, 4.0 TB/s; one row a warp took 25. 64 rows:
+// 4.3 us, a launch.
 constexpr int kRowsPerWarp = 4;
 
 template <int N>

@@ -555,10 +555,13 @@ __device__ __forceinline__ int tiles_before(const BlockSmem& sm, long long x) {
 // block that straddles prompts, or has a few rows of each) take their sequences'
 // tiles one after the other, with the groups that have a row of the sequence.
 //
-// 4096 rows x 16K keys: 277 us, 1.73 PFLOP/s. Without the sums and the stores 197;
-// the sums (a maximum a product, an FMA for two, eight loads of weights a row and key
-// quarter: ~70 instructions, 16 rows a scheduler and tile) need 1150 cycles a tile
-// beside the products' 1030 and get 64% of the issue slots. Accumulators of 256
+// 4096 rows x 16K keys: 280 us back to back, 1.72 PFLOP/s (318 as single calls). Two
+// things hold it. Without the sums and the stores it takes 197 us, twice the
+// products' own 1030 cycles a tile: an accumulator has no second buffer and is given
+// back only after four rounds of load, wait and sum, so the tensor cores wait for it
+// (the pipe is active 40 %). And the sums (a maximum a product, an FMA for two, eight
+// loads of weights a row and key quarter: ~70 instructions, 16 rows a scheduler and
+// tile) need 1150 issue cycles a tile, 64 % of the slots. Accumulators of 256
 // columns took 301 us, eight epilogue warps 365, x + |x| for half of the maxima 291.
 __global__ void __launch_bounds__(kBlkThreads, 1)
     fp8_index_block_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap map_q,

@@ -18,14 +18,24 @@
 //   - the weight u = p * s_i * 2^(2 - A), at most 128, k = 64: 8 significant
 //     bits, the precision of a bf16 weight, in steps of at least 2^-15 (2^-16 of
 //     the largest u of its frame: what is below is lost).
-// The frame A of each head follows the running maximum of log2(p s). It is m plus
-// an integer, m the largest logit where it was set, so that the heaviest key's u
-// is a power of two: a row of one key comes out exact. It is set from the first
-// tile, raised when a u would pass 128, and set anew every 16 tiles (also
-// downwards, to 2^-60 of the highest: O is then scaled up, fp32 has the range), so
-// that the loss stays relative to the 2048 keys around a key however long the list is. The sum of the
-// softmax is kept apart, in fp32, of the unrounded weights, in its own frame m (a
-// key's scale, which is no part of its weight, cannot disturb it).
+// The frame A of each head follows the running maximum of log2(p s). It is kept as
+// its distance from m, the largest logit where it was set: an integer, so that the
+// heaviest key's u is a power of two (a row of one key comes out exact), no lower
+// than -124, and changed with m also where no key of a tile adds to O. It is set
+// from the first tile, raised when a u would pass 128, and set anew every 16 tiles
+// (also downwards, to 2^-60 of the highest: O is then scaled up, fp32 has the
+// range), so that the loss stays relative to the 2048 keys around a key however long
+// the list is. The sum of the softmax is kept apart, in fp32, of the unrounded
+// weights, in its own frame m (a key's scale, which is no part of its weight, cannot
+// disturb it). Where a |m| passes 2^10 logits are rounded to fp32 before m is taken
+// from them, and the frame is set in two steps, m first.
+//
+// What the weights' steps cost: a key whose weight lies 2^-14 or more below the
+// largest keeps 3 bits or fewer. On rows of 2048 keys that a sink dominates (0.9 and
+// 0.99 of the weight) the output's error is that of its own bf16 rounding (1.7e-3);
+// relative to the other keys' part alone 0.144 where the rounding of the output
+// makes 0.137, and 1.86 where it makes 1.87. Steps finer by 1, 2 or 3 bits, at the
+// cost of the room to 128, take 3, 9 or 16 % more time (more frames set).
 //
 // Layout. One tile is 128 keys: S^T [128 keys x 64] = C Q^T (K = 576: 18
 // instructions), then O^T [512 dims x 64] += C^T P (4 x 4 instructions of 128
@@ -45,9 +55,9 @@
 // What bounds it. A tile's chain (copies ~2700 cycles, S ~1400, softmax ~1400, O
 // ~1200) over the ring of two; the products alone are 1650 (34 instructions at 48
 // cycles, held by the 6 KB of shared memory that each reads). Measured: 2048 rows of
-// 2048 keys, 2 sub-blocks: 1.00 ms, 585 TFLOP/s, ~4200 cycles a tile (the bf16
+// 2048 keys, 2 sub-blocks: 1.02 ms, 572 TFLOP/s, ~4300 cycles a tile (the bf16
 // kernel's rate for these products: ~2.4 ms); 130 rows of 1855 keys, one sub-block:
-// 45 us; 16 rows of 2048, 2 sub-blocks: 25 us and one row 14 us, of which 10 to 12
+// 46 us; 16 rows of 2048, 2 sub-blocks: 25 us and one row 14 us, of which 10 to 12
 // are the chain of one item (lookup, query, the first frame, output) and the join of
 // the splits.
 #include "fp8.cuh"
